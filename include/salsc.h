@@ -406,6 +406,117 @@ salsc_status salsc_shard_merge(const float* part_all, int32_t n_shards, int32_t 
                                void* ws, size_t ws_bytes, salsc_stream stream);
 
 /*
+ * Paged 8-bit cache of full keys and values, for the layers of a model that
+ * are not compressed (SALS page, abstract: latent keys keep their
+ * representation across most layers, so the others need an ordinary cache
+ * beside the latent one) and for prompts.  No counterpart in the SALS paper.
+ *
+ * A pool holds n_pages pages of page_size tokens for every KV head:
+ *   k_pages, v_pages   [n_pages][Hkv][page_size][d]  e4m3 codes (1 sign, 4
+ *                      exponent, 3 mantissa bits; NaN but no infinity)
+ *   k_scales, v_scales [n_pages][Hkv] fp32: a code stands for code * scale
+ * Keys are held after RoPE.  Token t of sequence b lies in slot t % page_size
+ * of page page_table[b][t / page_size], at RoPE position t.
+ *
+ * One step: sequence b has n_b = seq_lens[b] tokens in the cache, of which the
+ * last m_b = q_offsets[b+1] - q_offsets[b] are new in this step; their rows in
+ * K_new, V_new, q and out are q_offsets[b] .. q_offsets[b+1]-1.
+ * salsc_page_append writes them, salsc_page_attend attends from them.  n_b = 0
+ * and m_b = 0 are fine (an empty slot of a padded batch).  If m_b > n_b, the
+ * first m_b - n_b rows have no position: nothing is appended for them and
+ * their outputs are zeros.  Rows at or behind q_offsets[batch] are neither
+ * read nor written.
+ *
+ * The lengths, offsets and the page table are read on the device only, so a
+ * captured CUDA graph serves changing lengths.  They are checked there: an
+ * entry of the page table that is needed and outside 0 .. n_pages-1, a length
+ * outside 0 .. max_pages * page_size, offsets that decrease or pass n_tokens,
+ * and more than max_q new tokens set bit 0 of the workspace's anomaly word;
+ * tokens in a bad page are left out, lengths and offsets are cut to the
+ * bounds, and rows past max_q are left as they were.
+ */
+typedef struct {
+  int32_t batch;       /* B >= 1 */
+  int32_t n_q_heads;   /* Hq, a multiple of n_kv_heads, at most 16 per KV head */
+  int32_t n_kv_heads;  /* Hkv; query head h reads KV head h / (Hq / Hkv) */
+  int32_t head_dim;    /* d: 64 or 128 */
+  int32_t page_size;   /* tokens of a page: 16, 32, 64 or 128 */
+  int32_t n_pages;     /* pages of the pool; n_pages * Hkv * page_size < 2^31 */
+  int32_t max_pages;   /* row length of the page table; max_pages * page_size < 2^31 */
+  int32_t n_tokens;    /* rows of K_new, V_new, q and out, at least q_offsets[B] */
+  int32_t max_q;       /* most new tokens of one sequence (0: nothing is done) */
+  const int32_t* page_table_dev; /* [B][max_pages]; entries past a sequence's end are not read */
+  const int32_t* seq_lens_dev;   /* [B] tokens in the cache, this step's included */
+  const int32_t* q_offsets_dev;  /* [B+1], [0] >= 0; or NULL: row b is sequence b's one token */
+  double rope_base;    /* > 1, or 0: keys and queries are taken as they are (no rotation) */
+  float softmax_scale; /* 0 -> 1/sqrt(head_dim) */
+  int32_t window;      /* 0: a query sees every token up to its own position; W > 0: the last W */
+  salsc_dtype dtype;   /* storage type of K_new, V_new, q and out */
+} salsc_page_desc;
+
+/*
+ * Bytes of device workspace the two calls need for this descriptor (0 if it
+ * is invalid or unsupported); it depends on the descriptor's numbers only.
+ * One workspace serves any number of layers in stream order; calls that may
+ * overlap need one each.
+ */
+size_t salsc_page_workspace_size(const salsc_page_desc* desc);
+
+/* Clear the workspace's anomaly word (as salsc_decode_prepare); once per workspace. */
+salsc_status salsc_page_prepare(const salsc_page_desc* desc, void* ws, size_t ws_bytes,
+                                salsc_stream stream);
+
+/*
+ * Append this step's tokens: rotate the keys at their positions (rotate-half,
+ * as salsc_decode_step), and write keys and values as e4m3 codes.
+ * For every page and KV head written, with a the largest size of its new
+ * tokens (|k_i| + |k_{i+d/2}| for rotated keys, which bounds the pair at every
+ * position; |k| or |v| otherwise; values that are not finite do not count):
+ *   scale = the least power of two with a <= 448 * scale (at least 2^-100);
+ *           where the page holds earlier tokens (slots before the first new
+ *           one), the larger of that and the page's scale
+ *   code  = the e4m3 number nearest to value / scale (ties to even;
+ *           infinities become +-448, NaN stays)
+ * Where the scale grew, the earlier tokens' codes are recoded with it; a power
+ * of two only rounds those that fall below e4m3's normal range again.  Slots
+ * behind the new tokens keep their bytes.
+ *
+ *   K_new, V_new  [n_tokens][Hkv][d], rows k_stride and v_stride elements
+ *                 apart (0: contiguous; otherwise a multiple of 8, at least
+ *                 Hkv*d), 16-byte aligned
+ * A page written by this step belongs to one sequence, once (not checked).
+ * Allocates nothing, stream-ordered, graph-capturable; launched with
+ * programmatic dependent launch, reading nothing before earlier work is done.
+ * Errors: INVALID_ARG (descriptor, null or misaligned pointers, strides),
+ * UNSUPPORTED (head_dim, page_size, heads per KV head, pool size), WORKSPACE,
+ * CUDA.
+ */
+salsc_status salsc_page_append(const salsc_page_desc* desc, const void* K_new, int64_t k_stride,
+                               const void* V_new, int64_t v_stride, void* k_pages, void* v_pages,
+                               float* k_scales, float* v_scales, void* ws, size_t ws_bytes,
+                               salsc_stream stream);
+
+/*
+ * Attention of this step's tokens over their sequences' pages:
+ *   out[i,h] = sum_t softmax_t(RoPE(q[i,h], p) . K_t * softmax_scale) V_t
+ * over the tokens t <= p (and t > p - window) of the sequence, for the row's
+ * position p = n_b - m_b + i; zeros where there is none.  K_t and V_t are the
+ * values that the pages hold.
+ *
+ *   q    [n_tokens][Hq][d] before RoPE, rows q_stride elements apart (0:
+ *        contiguous; otherwise a multiple of 8, at least Hq*d), 16-byte aligned
+ *   out  [n_tokens][Hq][d] contiguous, 16-byte aligned, apart from the inputs
+ * What lies in slots past a sequence's end does not matter (NaN included).
+ * Allocates nothing, stream-ordered, graph-capturable; launched with
+ * programmatic dependent launch, reading nothing before earlier work is done.
+ * Errors: as salsc_page_append.
+ */
+salsc_status salsc_page_attend(const salsc_page_desc* desc, const void* q, int64_t q_stride,
+                               const void* k_pages, const void* v_pages, const float* k_scales,
+                               const float* v_scales, void* out, void* ws, size_t ws_bytes,
+                               salsc_stream stream);
+
+/*
  * Device-side anomaly flags recorded in a workspace since salsc_decode_prepare
  * (bit 0: a selected index fell outside its sequence; bit 1: a pipeline wait
  * gave up after its iteration limit).  Copies one word to *flags_host and

@@ -28,7 +28,8 @@ EXPORTS = (
     "salsc_decode_launch_count", "salsc_append", "salsc_decode_step_append",
     "salsc_fit_workspace_size",
     "salsc_fit_projection", "salsc_shard_candidates", "salsc_shard_select", "salsc_shard_attend",
-    "salsc_shard_merge", "salsc_check_wait_timeout", "salsc_decode_read_flags",
+    "salsc_shard_merge", "salsc_page_workspace_size", "salsc_page_prepare", "salsc_page_append",
+    "salsc_page_attend", "salsc_check_wait_timeout", "salsc_decode_read_flags",
     "salsc_status_string", "salsc_last_cuda_error",
     "salsc_version",
 )
@@ -59,6 +60,27 @@ class DecodeDesc(ctypes.Structure):
         ("dtype", ctypes.c_int),
         ("select_mode", ctypes.c_int32),
         ("select_threshold", ctypes.c_float),
+    ]
+
+
+class PageDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("max_q", ctypes.c_int32),
+        ("page_table_dev", ctypes.c_void_p),
+        ("seq_lens_dev", ctypes.c_void_p),
+        ("q_offsets_dev", ctypes.c_void_p),
+        ("rope_base", ctypes.c_double),
+        ("softmax_scale", ctypes.c_float),
+        ("window", ctypes.c_int32),
+        ("dtype", ctypes.c_int),
     ]
 
 
@@ -111,6 +133,15 @@ def _lib():
         lib.salsc_decode_step_static_ws.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.salsc_static_workspace_bytes.restype = sz
         lib.salsc_static_workspace_bytes.argtypes = []
+        pp = ctypes.POINTER(PageDesc)
+        lib.salsc_page_workspace_size.restype = sz
+        lib.salsc_page_workspace_size.argtypes = [pp]
+        lib.salsc_page_prepare.restype = ctypes.c_int
+        lib.salsc_page_prepare.argtypes = [pp, vp, sz, vp]
+        lib.salsc_page_append.restype = ctypes.c_int
+        lib.salsc_page_append.argtypes = [pp, vp, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+        lib.salsc_page_attend.restype = ctypes.c_int
+        lib.salsc_page_attend.argtypes = [pp, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp]
         lib.salsc_check_wait_timeout.restype = ctypes.c_int
         lib.salsc_check_wait_timeout.argtypes = [ctypes.c_uint64, vp, sz, vp]
         lib.salsc_decode_read_flags.restype = ctypes.c_int
@@ -410,3 +441,114 @@ class Decoder:
 
     def flags(self, stream=None) -> int:
         return salsc_decode_read_flags(self.ws, stream)
+
+
+def alloc_pages(n_pages, n_kv_heads, page_size, head_dim, device="cuda"):
+    """An empty paged cache of one layer: (k_pages, v_pages, k_scales, v_scales), e4m3 codes
+    [n_pages][n_kv_heads][page_size][head_dim] and fp32 scales [n_pages][n_kv_heads]."""
+    shape = (n_pages, n_kv_heads, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+    return k, v, ks, vs
+
+
+class PagedCache:
+    """Descriptor + workspace of one step over paged 8-bit caches (include/salsc.h, salsc_page_*).
+
+    ``page_table`` int32 [batch][max_pages], ``seq_lens`` int32 [batch] (this step's tokens
+    included) and ``q_offsets`` int32 [batch+1] (None: one new token of each sequence) are CUDA
+    tensors that the calls read; writing new lengths and pages into them serves the next step
+    with the same object, or a captured graph's next replay.  ``n_tokens`` is the number of rows
+    of the step's tensors (default: batch), ``max_q`` the most new tokens of one sequence.
+    The pools of a layer (alloc_pages) are passed per call: one object serves every layer, in
+    stream order.
+    """
+
+    def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, page_table, seq_lens,
+                 q_offsets=None, n_tokens=None, max_q=1, rope_base=10000.0, softmax_scale=0.0,
+                 window=0, dtype=torch.bfloat16):
+        batch, max_pages = page_table.shape
+        for name, t, shape in (("page_table", page_table, (batch, max_pages)),
+                               ("seq_lens", seq_lens, (batch,)),
+                               ("q_offsets", q_offsets, (batch + 1,))):
+            if t is None and name == "q_offsets":
+                continue
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+            if t.device != page_table.device or not t.is_cuda:
+                raise ValueError(f"{name} must be on the page table's CUDA device")
+        self._held = (page_table, seq_lens, q_offsets)  # the descriptor points into them
+        self.page_table, self.seq_lens, self.q_offsets = self._held
+        self.device, self.dtype = page_table.device, dtype
+        self.n_tokens = batch if n_tokens is None else int(n_tokens)
+        self.kv_shape = (self.n_tokens, n_kv_heads, head_dim)
+        self.q_shape = (self.n_tokens, n_q_heads, head_dim)
+        self.pool_shape = (n_pages, n_kv_heads, page_size, head_dim)
+        self.desc = PageDesc(batch, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages,
+                             self.n_tokens, max_q, page_table.data_ptr(), seq_lens.data_ptr(),
+                             None if q_offsets is None else q_offsets.data_ptr(), float(rope_base),
+                             float(softmax_scale), window, _dtype_code(dtype))
+        self._desc = ctypes.byref(self.desc)
+        nbytes = int(_lib().salsc_page_workspace_size(self._desc))
+        if nbytes == 0:
+            raise SalscError(SALSC_ERR_INVALID_ARG, "salsc_page_workspace_size")
+        self.ws = alloc_workspace(nbytes, self.device)
+        self._ws = (self.ws.data_ptr(), nbytes)
+        with torch.cuda.device(self.device):
+            _check(_lib().salsc_page_prepare(self._desc, *self._ws, _stream(None)),
+                   "salsc_page_prepare")
+
+    def _rows(self, name, t, shape):
+        """Check a [n_tokens][heads][d] tensor; its row stride in elements."""
+        if t.dtype != self.dtype or t.device != self.device or t.shape != shape:
+            raise ValueError(f"{name} must be {self.dtype} {shape} on {self.device}")
+        stride = t.stride()
+        if stride[2] != 1 or stride[1] != shape[2]:
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        return stride[0] if shape[0] > 1 else 0
+
+    def _pools(self, pools):
+        for i, t in enumerate(pools):
+            dt, shape = ((torch.float8_e4m3fn, self.pool_shape) if i < 2
+                         else (torch.float32, self.pool_shape[:2]))
+            if (t.dtype != dt or t.device != self.device or t.shape != shape
+                    or not t.is_contiguous()):
+                raise ValueError(f"pools must be contiguous {dt} {shape} on {self.device}")
+        return [t.data_ptr() for t in pools]
+
+    def _call(self, fn, what, stream, *args):
+        if torch.cuda.current_device() == self.device.index:
+            s = stream if stream is not None else torch.cuda.current_stream()
+            st = fn(self._desc, *args, *self._ws, s.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                s = stream if stream is not None else torch.cuda.current_stream()
+                st = fn(self._desc, *args, *self._ws, s.cuda_stream)
+        if st != SALSC_OK:
+            raise SalscError(st, what)
+
+    def append(self, K_new, V_new, k_pages, v_pages, k_scales, v_scales, stream=None):
+        """Rotate, quantise and write this step's keys and values [n_tokens][n_kv_heads][d]
+        (rows may be strided, as in a fused projection's output) into the pages."""
+        ks, vs = self._rows("K_new", K_new, self.kv_shape), self._rows("V_new", V_new, self.kv_shape)
+        self._call(_lib().salsc_page_append, "salsc_page_append", stream, K_new.data_ptr(), ks,
+                   V_new.data_ptr(), vs, *self._pools((k_pages, v_pages, k_scales, v_scales)))
+
+    def attend(self, q, k_pages, v_pages, k_scales, v_scales, out=None, stream=None):
+        """Attention of this step's queries [n_tokens][n_q_heads][d] (before RoPE; rows may be
+        strided) over their sequences' pages; rows of no sequence are left as they were."""
+        qs = self._rows("q", q, self.q_shape)
+        if out is None:
+            out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
+        elif (out.dtype != self.dtype or out.device != self.device or out.shape != self.q_shape
+                or not out.is_contiguous()):
+            raise ValueError(f"out must be contiguous {self.dtype} {self.q_shape}")
+        self._call(_lib().salsc_page_attend, "salsc_page_attend", stream, q.data_ptr(), qs,
+                   *self._pools((k_pages, v_pages, k_scales, v_scales)), out.data_ptr())
+        return out
+
+    def flags(self, stream=None) -> int:
+        """The workspace's anomaly word (synchronises the stream)."""
+        with torch.cuda.device(self.device):
+            return salsc_decode_read_flags(self.ws, stream)
