@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "page_sched.cuh"
 
 namespace salsc {
 
@@ -120,7 +121,139 @@ __device__ __forceinline__ void page_cs(int pos, double turns, float& c, float& 
   sincospif((float)(2.0 * (a - rint(a))), &s, &c);
 }
 
+// ---------------------------------------------------------------- attention
+
+// Which sequences a kernel of the attention takes, and how it cuts them.
+struct PageWork {
+  int min_rows, max_rows;  // sequences with min_rows <= new tokens * G <= max_rows
+  int tb;                  // new tokens of a row block
+  int rows;                // rows of a partial slot (>= tb * G)
+  // Partial results of units that several CTAs share: CTA c's slots 2c (a
+  // piece that starts inside a unit) and 2c + 1 (one that starts a unit and
+  // does not end it), of `rows` rows each
+  float* acc;     // [2 * grid][rows][d] unnormalised outputs
+  float2* ml;     // [2 * grid][rows] running maximum (log2 units) and normaliser
+  int4* info;     // [grid] of slot 2c + 1: first row's token row, KV head, rows, last CTA of the unit
+};
+
+// A cursor over the step's units and tiles, for one warp or thread (every
+// thread that uses one advances it alike).
+struct PageCursor {
+  const PageStep& s;
+  const PageWork& w;
+  int b, u, k;      // sequence, KV head, row block
+  PageBlocks blk;   // of sequence b
+  int row0;         // row of the sequence's first new token
+  int tiles;        // tiles of the unit
+  int tile;         // tile inside the unit (0-based from the block's first tile)
+
+  __device__ __forceinline__ PageCursor(const PageStep& s_, const PageWork& w_) : s(s_), w(w_) {}
+  __device__ __forceinline__ void load() {
+    const PageSeq q = page_seq(s, b);
+    blk = PageBlocks{q.n, q.m, w.tb, s.window};
+    row0 = q.row0;
+  }
+  __device__ __forceinline__ bool mine() const {
+    const int64_t r = (int64_t)blk.m * s.G;
+    return r >= w.min_rows && r <= w.max_rows;
+  }
+  // to the next unit; false past the last one
+  __device__ __forceinline__ bool next_unit() {
+    tile = 0;
+    if (++u < s.U) return true;
+    u = 0;
+    if (++k < blk.count()) {
+      tiles = blk.tiles(k);
+      return true;
+    }
+    k = 0;
+    while (++b < s.B) {
+      load();
+      if (mine()) {
+        tiles = blk.tiles(0);
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int64_t page_seq_tiles(const PageStep& s, const PageWork& w, int b) {
+  const PageSeq q = page_seq(s, b);
+  const int64_t r = (int64_t)q.m * s.G;
+  if (r < w.min_rows || r > w.max_rows) return 0;
+  const PageBlocks p{q.n, q.m, w.tb, s.window};
+  return (int64_t)s.U * p.before(p.count());
+}
+
+// Block-wide: the total number of tiles of the kernel's sequences, this CTA's
+// range of them [x0, x1), and where x0 lies (b, and the tile's index within
+// sequence b); b = -1 for an empty range.  sm: (blockDim / 32 + 2) int64.
+__device__ __forceinline__ void page_share(const PageStep& s, const PageWork& w, int64_t* sm,
+                                           int64_t& total, int64_t& x0, int64_t& x1, int& b,
+                                           int64_t& rem) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  total = 0;
+  // one pass for the total, a second one (from cached lengths) for the place;
+  // with one round of threads the first pass's counts are kept
+  int64_t mine = 0, end = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t run = 0;
+    if (pass == 1) {
+      x0 = share_begin(blockIdx.x, total, gridDim.x);
+      x1 = share_begin(blockIdx.x + 1, total, gridDim.x);
+      b = -1;
+      rem = 0;
+      if (x0 >= x1) return;
+    }
+    for (int b0 = 0; b0 < s.B; b0 += blockDim.x) {
+      if (pass == 0 || s.B > (int)blockDim.x) {
+        mine = b0 + tid < s.B ? page_seq_tiles(s, w, b0 + tid) : 0;
+        int64_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += t;
+        }
+        __syncthreads();
+        if (lane == 31) sm[warp] = inc;
+        __syncthreads();
+        int64_t before = run;
+        for (int i = 0; i < warps; ++i) {
+          if (i < warp) before += sm[i];
+          run += sm[i];
+        }
+        end = before + inc;
+      }
+      if (pass == 1 && x0 >= end - mine && x0 < end) {
+        sm[warps] = b0 + tid;
+        sm[warps + 1] = x0 - (end - mine);
+      }
+    }
+    if (pass == 0) {
+      total = run;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  b = (int)sm[warps];
+  rem = sm[warps + 1];
+}
+
+// Place a cursor on tile `rem` of sequence b.
+__device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem) {
+  c.b = b;
+  c.load();
+  // the row block: its U KV heads have U * tiles(k) tiles behind U * before(k)
+  c.k = c.blk.block_of(rem / c.s.U);
+  c.tiles = c.blk.tiles(c.k);
+  rem -= (int64_t)c.s.U * c.blk.before(c.k);
+  c.u = (int)(rem / c.tiles);
+  c.tile = (int)(rem % c.tiles);
+}
+
 // Host side: launchers.
+constexpr int kPageGrid = 148;  // CTAs of the attention kernels: one per SM
 cudaError_t launch_page_append(const PageStep& s, const void* K, int64_t k_stride, const void* V,
                                int64_t v_stride, void* k_pages, void* v_pages, float* k_scales,
                                float* v_scales, salsc_dtype dt, cudaStream_t stream);
@@ -129,5 +262,12 @@ cudaError_t launch_page_attend(const PageStep& s, const void* q, int64_t q_strid
                                const float* v_scales, void* out, void* part, salsc_dtype dt,
                                cudaStream_t stream);
 size_t page_attend_workspace(const PageStep& s, salsc_dtype dt);
+// The attention of few rows (page_few.cu): rows of its row blocks, and its launch.
+int page_few_rows(const PageStep& s, salsc_dtype dt);
+cudaError_t launch_page_few(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
+                            const void* k_pages, const void* v_pages, const float* k_scales,
+                            const float* v_scales, void* out, salsc_dtype dt, cudaStream_t stream);
+cudaError_t launch_page_merge(const PageStep& s, const PageWork& w, void* out, salsc_dtype dt,
+                              cudaStream_t stream);
 
 }  // namespace salsc

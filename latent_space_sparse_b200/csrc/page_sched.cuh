@@ -1,0 +1,97 @@
+// page_sched.cuh -- the paged attention's work list: which tiles of keys each
+// block of query rows needs, and where the i-th tile of the step lies.
+//
+// A unit is (sequence, row block, KV head): a row block is `tb` consecutive
+// new tokens with all the query heads of the KV head, and its tiles are the
+// 128-token tiles that any of its rows sees (one tile at least, so that rows
+// that see nothing have somebody to write their zeros).  Tiles are numbered
+// in the order sequence, row block, KV head, tile; CTAs take contiguous
+// ranges of equal length, so no sizes need to be known on the host.  All of
+// it is integer arithmetic on a sequence's length and number of new tokens.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SALSC_HD __host__ __device__ __forceinline__
+#else
+#define SALSC_HD inline
+#endif
+
+namespace salsc {
+
+constexpr int kPageTile = 128;  // tokens of a key tile
+
+// sum over i < n of floor((a*i + b) / m), for n, a, b >= 0, m > 0, by the
+// Euclidean reduction of (a, m).
+SALSC_HD int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// One sequence's row blocks: n tokens in the cache, the last m of them new (m
+// may exceed n), blocks of tb new tokens, window w (0: none).
+struct PageBlocks {
+  int n, m, tb, w;
+
+  SALSC_HD int count() const { return m / tb + (m % tb != 0); }
+  // positions of the first and last row of block k (negative: no position)
+  SALSC_HD int pos0(int k) const { return n - m + k * tb; }
+  SALSC_HD int pos1(int k) const {
+    const int left = m - k * tb;
+    return n - m + k * tb + (tb < left ? tb : left) - 1;
+  }
+  // first token that block k sees, and its first tile
+  SALSC_HD int lo(int k) const {
+    const int64_t x = (int64_t)pos0(k) - w + 1;
+    return w && x > 0 ? (int)x : 0;
+  }
+  SALSC_HD int tile0(int k) const { return lo(k) / kPageTile; }
+  SALSC_HD int tiles(int k) const {
+    const int p = pos1(k);
+    return (p > 0 ? p / kPageTile : 0) - tile0(k) + 1;
+  }
+  // sum over blocks i < k of max(c + i*tb, 0) / 128
+  SALSC_HD int64_t ramp(int64_t c, int64_t k) const {
+    int64_t r0 = 0;
+    if (c < 0) r0 = (-c + tb - 1) / tb;
+    return r0 < k ? floor_sum(k - r0, kPageTile, tb, c + r0 * tb) : 0;
+  }
+  // tiles of blocks 0 .. k-1
+  SALSC_HD int64_t before(int k) const {
+    const int nb = count();
+    if (k <= 0) return 0;
+    if (nb == 1) return tiles(0);
+    const int full = k < nb ? k : nb - 1;
+    int64_t s = ramp((int64_t)n - m + tb - 1, full) + k;
+    if (k == nb) s += (n > 1 ? n - 1 : 0) / kPageTile;
+    if (w) s -= ramp((int64_t)n - m - w + 1, k);
+    return s;
+  }
+  // the block that holds tile x of one KV head's tiles (0 <= x < before(count()))
+  SALSC_HD int block_of(int64_t x) const {
+    int a = 0, b = count() - 1;
+    while (a < b) {
+      const int c = (a + b + 1) / 2;
+      if (before(c) <= x)
+        a = c;
+      else
+        b = c - 1;
+    }
+    return a;
+  }
+};
+
+}  // namespace salsc

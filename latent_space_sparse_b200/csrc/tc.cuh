@@ -165,6 +165,17 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (8-bit inputs, fp32 accumulate).
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // One lane of the (converged) warp: the issuer of a single-thread operation
 // whose operands the whole warp computed.
 __device__ __forceinline__ bool elect_one() {
@@ -276,6 +287,15 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          | ((uint32_t)(M >> 4) << 24); // M / 16
 }
 
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B, fp32 D, shape M x N;
+// A K-major or (amn) MN-major, B K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool amn) {
+  return (1u << 4)                    // D format f32; A and B format 0: e4m3
+         | ((amn ? 1u : 0u) << 15)
+         | ((uint32_t)(N >> 3) << 17)
+         | ((uint32_t)(M >> 4) << 24);
+}
+
 // Instruction descriptor: bf16 A stored MN-major, bf16 B K-major, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32_amn(int M, int N) {
   return idesc_bf16_f32(M, N) | (1u << 15);
@@ -298,6 +318,20 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t addr, uint32_t 
   d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// Shared-memory descriptor of an operand in the 64-byte swizzled layout (rows
+// of 64 bytes, 8 rows per 512-byte atom).  K-major: sbo = byte distance of
+// 8-row groups.  MN-major: lbo between 64-byte MN blocks, sbo between 8-row K
+// groups.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)4u << 61;
   return d;
 }
 
@@ -364,6 +398,19 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t (&v)[2]) {
                : "r"(taddr));
 }
 
+// Registers -> TMEM: 32 lanes x 16 (8) columns of 32-bit, and the wait for such stores.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -377,5 +424,10 @@ __device__ __forceinline__ void tmem_ld_wait() {
 // swizzle).  Returns false (and leaves *map untouched) on failure.
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows, uint32_t box_cols);
+
+// The same for a matrix of bytes [rows][cols], cols = 64 or 128, whole rows to
+// a box, swizzled over 64 or 128 bytes.
+bool make_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t cols,
+                       uint32_t box_rows);
 
 }  // namespace salsc

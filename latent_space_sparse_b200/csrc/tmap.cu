@@ -42,4 +42,23 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64
   return true;
 }
 
+bool make_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t cols,
+                       uint32_t box_rows) {
+  std::call_once(g_once, load_encode);
+  if (!g_encode) return false;
+  if (((uintptr_t)base & 15u) || (cols != 64 && cols != 128)) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols};
+  cuuint32_t box[2] = {cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUtensorMap m;
+  CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return false;
+  *map = m;
+  return true;
+}
+
 }  // namespace salsc
