@@ -240,16 +240,26 @@ __device__ __forceinline__ void page_share(const PageStep& s, const PageWork& w,
   rem = sm[warps + 1];
 }
 
-// Place a cursor on tile `rem` of sequence b.
+// Place a cursor on tile `rem` of sequence b.  Every lane of the warp calls it,
+// with the same arguments: the row block is found by 32 tries at a time.
 __device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem) {
   c.b = b;
   c.load();
   // the row block: its U KV heads have U * tiles(k) tiles behind U * before(k)
-  c.k = c.blk.block_of(rem / c.s.U);
+  const int64_t x = div_small(rem, c.s.U);
+  int lo = 0, n = c.blk.count();  // the block is one of lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, k = lo + (int)(threadIdx.x & 31) * step;
+    const bool at = k < lo + n && c.blk.before(k) <= x;
+    const int hit = __popc(__ballot_sync(0xffffffffu, at)) - 1;  // before() grows with k
+    n = min(step, n - hit * step);
+    lo += hit * step;
+  }
+  c.k = lo;
   c.tiles = c.blk.tiles(c.k);
   rem -= (int64_t)c.s.U * c.blk.before(c.k);
-  c.u = (int)(rem / c.tiles);
-  c.tile = (int)(rem % c.tiles);
+  c.u = (int)div_small(rem, c.tiles);
+  c.tile = (int)(rem - (int64_t)c.u * c.tiles);
 }
 
 // Host side: launchers.
@@ -267,6 +277,11 @@ int page_few_rows(const PageStep& s, salsc_dtype dt);
 cudaError_t launch_page_few(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
                             const void* k_pages, const void* v_pages, const float* k_scales,
                             const float* v_scales, void* out, salsc_dtype dt, cudaStream_t stream);
+// The attention of many rows (page_many.cu; bf16): rows of its row blocks, and its launch.
+constexpr int kPageManyRows = 256;
+cudaError_t launch_page_many(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
+                             const void* k_pages, const void* v_pages, const float* k_scales,
+                             const float* v_scales, void* out, cudaStream_t stream);
 cudaError_t launch_page_merge(const PageStep& s, const PageWork& w, void* out, salsc_dtype dt,
                               cudaStream_t stream);
 

@@ -67,28 +67,51 @@ page_merge_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pa
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-PageWork layout(const PageStep& s, int rows, void* part, size_t* bytes) {
+// Partial results of a kernel whose row blocks have `rows` rows, from p + off on; off moves behind
+// them.
+PageWork layout(const PageStep& s, int rows, void* part, size_t& off) {
   PageWork w{};
   w.rows = rows;
-  w.tb = rows / s.G;
   char* p = (char*)part;
-  size_t off = 0;
   w.info = (int4*)(p + off);
   off = align_up(off + sizeof(int4) * kPageGrid);
   w.ml = (float2*)(p + off);
   off = align_up(off + sizeof(float2) * 2 * kPageGrid * rows);
   w.acc = (float*)(p + off);
   off = align_up(off + sizeof(float) * 2 * kPageGrid * rows * s.d);
-  *bytes = off;
   return w;
+}
+
+// The kernels of a step: sequences with at most `few.max_rows` rows per KV head
+// go to page_few, the others (bf16 only) to page_many.
+struct Plan {
+  PageWork few, many;
+  bool has_many;
+  size_t bytes;
+};
+
+Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
+  Plan p{};
+  const int rows = page_few_rows(s, dt);
+  p.few = layout(s, rows, part, p.bytes);
+  p.few.tb = rows / s.G;
+  p.few.min_rows = 1;
+  p.few.max_rows = INT32_MAX;
+  p.has_many = dt == SALSC_BF16 && (int64_t)s.max_q * s.G > rows;
+  if (p.has_many) {
+    p.many = layout(s, kPageManyRows, part, p.bytes);
+    p.many.tb = 2 * (kPageManyRows / 2 / s.G);
+    p.many.min_rows = rows + 1;
+    p.many.max_rows = INT32_MAX;
+    p.few.max_rows = rows;
+  }
+  return p;
 }
 
 }  // namespace
 
 size_t page_attend_workspace(const PageStep& s, salsc_dtype dt) {
-  size_t n;
-  layout(s, page_few_rows(s, dt), nullptr, &n);
-  return n;
+  return make_plan(s, dt, nullptr).bytes;
 }
 
 cudaError_t launch_page_merge(const PageStep& s, const PageWork& w, void* out, salsc_dtype dt,
@@ -110,14 +133,16 @@ cudaError_t launch_page_attend(const PageStep& s, const void* q, int64_t q_strid
                                const void* k_pages, const void* v_pages, const float* k_scales,
                                const float* v_scales, void* out, void* part, salsc_dtype dt,
                                cudaStream_t stream) {
-  size_t bytes;
-  PageWork w = layout(s, page_few_rows(s, dt), part, &bytes);
-  w.min_rows = 1;
-  w.max_rows = INT32_MAX;
-  const cudaError_t e = launch_page_few(s, w, q, q_stride, k_pages, v_pages, k_scales, v_scales,
-                                        out, dt, stream);
-  if (e != cudaSuccess) return e;
-  return launch_page_merge(s, w, out, dt, stream);
+  const Plan p = make_plan(s, dt, part);
+  cudaError_t e = cudaSuccess;
+  if (p.has_many) {
+    e = launch_page_many(s, p.many, q, q_stride, k_pages, v_pages, k_scales, v_scales, out, stream);
+    if (e == cudaSuccess) e = launch_page_merge(s, p.many, out, dt, stream);
+  }
+  if (e == cudaSuccess)
+    e = launch_page_few(s, p.few, q, q_stride, k_pages, v_pages, k_scales, v_scales, out, dt, stream);
+  if (e == cudaSuccess) e = launch_page_merge(s, p.few, out, dt, stream);
+  return e;
 }
 
 }  // namespace salsc

@@ -179,13 +179,11 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               // value scale f * 2^e; zeros and what is not finite keep e = 0
               int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
               if (e < -100 || e > 100) e = 0;
-              const float up = __uint_as_float((uint32_t)(127 + e) << 23);
               const float down = __uint_as_float((uint32_t)(127 - e) << 23);
               meta[st].ks[sub] = ks;
               meta[st].vf[sub] = vs * down;
               meta[st].ve[sub] = (float)e;
               meta[st].ive[sub] = down;
-              (void)up;
               if (sub == 0) meta[st].loaded = got >> (npg * (i - i0));
             }
             __syncwarp();
@@ -274,7 +272,6 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         const int any_lo = cur.blk.lo(cur.k);
 
         // the rows' terms: a warp per row
-        named_rows:
         for (int r = warp; r < RC; r += 4) {
           const int i = r / s.G, g = r - i * s.G;
           float x2[D / 64][2];

@@ -1,0 +1,594 @@
+// page_many.cu -- attention of many query rows over the paged 8-bit cache
+// (prompts and chunks of prompts, bf16 storage).
+//
+//   s_t = RoPE(q) . K_t,  p = softmax(scale * s),  out = sum_t p_t V_t
+//
+// A row block is two halves of 128 rows: each half the query heads of one KV
+// head for floor(128 / G) consecutive new tokens.  Per tile of 128 tokens and
+// half, on tcgen05 kind::f16 with fp32 accumulators in TMEM:
+//   S [128 x 128 tokens]  = Q (K-major)         x  K tile (K-major)
+//   O [128 x d]          += P (A from TMEM)     x  V tile (MN-major)
+// e4m3 codes are exact in f16, which also gives the rotated queries and the
+// weights 11 bits.  Codes are read once per tile and both halves use them.
+//
+// Scales: a page's key scale multiplies its scores; its value scale
+// v = f * 2^e, 1 <= f < 2, enters the softmax as t = s + e (log2 units) and
+// the normaliser as p * 2^-e; f and both scales' signs go into the f16 values.
+// So the weights 2^(t - m) stay in f16's range whatever the scales are.
+//
+// The maximum that the weights refer to follows the rows' maximum only when
+// that has grown by more than kSlack: weights up to 2^kSlack hold as well in
+// f16, and O is rescaled a few times in a row's life and not once per tile.
+//
+// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of a half (a
+// thread per row), warps 8-11 queries (rotation, f16) and cache tiles (codes
+// to f16, global to shared memory), warp 12 issues the MMAs.
+#include "page.cuh"
+#include "tc.cuh"
+
+namespace salsc {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kConvert = 128;   // threads of the converting warps
+constexpr int kRing = 8;        // tiles' scales that are kept
+constexpr float kSlack = 8.f;   // log2 units
+
+struct TileScales {
+  float ks[8], ve[8], ive[8];  // by group of 16 tokens: |key scale|, e, 2^-e
+  uint32_t loaded;             // groups that were loaded (bits)
+  uint32_t nan[4];             // tokens whose values hold a NaN, where rows differ in what they see
+};
+
+template <int D>
+struct Many {
+  static constexpr int kQHalf = 128 * D * 2;  // bytes
+  static constexpr int kTileBytes = kPageTile * D * 2;
+  static constexpr int kOffK = 2 * kQHalf;
+  static constexpr int kOffV = kOffK + 2 * kTileBytes;
+  static constexpr int kSmem = kOffV + 2 * kTileBytes + 1024;  // + alignment
+  static constexpr int kTmem = 512;
+  static constexpr int kColO = 256;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 16 e4m3 codes -> 16 f16 in two chunks.
+__device__ __forceinline__ void widen16(const uint4& c, uint32_t (&w)[8]) {
+  const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[i] & 0xFFFFu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[i] >> 16), __NV_E4M3);
+    w[2 * i] = (uint32_t)a.x | ((uint32_t)a.y << 16);
+    w[2 * i + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
+  }
+}
+
+// A byte of w is the NaN code 0x7F or 0xFF.
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *(const uint32_t*)&h;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
+                 const __nv_bfloat16* __restrict__ q, int64_t q_stride,
+                 const uint8_t* __restrict__ k_pages, const uint8_t* __restrict__ v_pages,
+                 const float* __restrict__ k_scales, const float* __restrict__ v_scales,
+                 __nv_bfloat16* __restrict__ out) {
+  using C = Many<D>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ TileScales meta[kRing];
+  __shared__ alignas(8) uint64_t bars[16];
+  __shared__ int64_t share[kThreads / 32 + 2];
+  __shared__ float qfac[2][256];  // by segment parity: softmax scale * log2(e) / the row's power of two
+  __shared__ uint32_t tmem_base;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t sm0 = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (sm0 - tc::smem_u32(smem_raw));
+  const uint32_t bar0 = tc::smem_u32(bars);
+  auto kfull = [&](int i) { return bar0 + 8u * i; };
+  auto kfree = [&](int i) { return bar0 + 8u * (2 + i); };
+  auto vfull = [&](int i) { return bar0 + 8u * (4 + i); };
+  auto vfree = [&](int i) { return bar0 + 8u * (6 + i); };
+  auto sready = [&](int h) { return bar0 + 8u * (8 + h); };
+  auto pready = [&](int h) { return bar0 + 8u * (10 + h); };
+  auto odone = [&](int h) { return bar0 + 8u * (12 + h); };
+  const uint32_t qfull = bar0 + 8u * 14, qfree = bar0 + 8u * 15;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(kfull(i), kConvert);
+      tc::mbar_init(kfree(i), 1);
+      tc::mbar_init(vfull(i), kConvert);
+      tc::mbar_init(vfree(i), 1);
+      tc::mbar_init(sready(i), 2);  // the scores, and the issuer for what it has waited for
+      tc::mbar_init(pready(i), 128);
+      tc::mbar_init(odone(i), 1);
+    }
+    tc::mbar_init(qfull, kConvert);
+    tc::mbar_init(qfree, 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == 12) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
+  if (tid < kRing * 4) meta[tid / 4].nan[tid % 4] = 0;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  int64_t total, x0, x1, rem;
+  int b;
+  page_share(s, w, share, total, x0, x1, b, rem);
+  if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base;
+  bool dead = false;  // a wait gave up: skip the others, so that the kernel ends
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (!dead && !tc::mbar_wait(bar, parity, s.flags)) dead = true;
+  };
+  const int tb2 = w.tb / 2;  // new tokens of a half
+
+  if (x0 < x1) {
+    PageCursor cur(s, w);
+    page_seek(cur, b, rem);
+    int64_t left = x1 - x0;
+    int it = 0;  // tiles so far
+    // tiles of the current segment; a segment is a piece of one unit
+    auto seg_tiles = [&] { return (int)min((int64_t)(cur.tiles - cur.tile), left); };
+    // 184 * 256 + 104 * 128 + 40 * 128 = 128 * 512 registers
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+      // ------------------------------------------------ MMA issuer
+      if (warp == 12 && tc::elect_one()) {
+        constexpr uint32_t id_s = tc::idesc_f16_f32(128, kPageTile, false);
+        constexpr uint32_t id_o = tc::idesc_f16_f32(128, D, true);
+        int cnt[2] = {0, 0};
+        auto scores = [&](int h, int i) {
+          const uint32_t k = sm0 + C::kOffK + (uint32_t)(i & 1) * C::kTileBytes;
+          const uint32_t qa = sm0 + (uint32_t)h * C::kQHalf;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk / 4) * 16384 + (kk % 4) * 32;
+            tc::mma_bf16(tmem + h * 128, tc::sdesc_kmajor_sw128(qa + off),
+                         tc::sdesc_kmajor_sw128(k + off), id_s, kk > 0);
+          }
+          tc::mma_commit(sready(h));
+          tc::mbar_arrive(sready(h));
+        };
+        auto values = [&](int h, int i, bool first) {
+          const uint32_t v = sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes;
+          wait(pready(h), cnt[h]++ & 1);
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < kPageTile / 16; ++kk)
+            tc::mma_f16_ts(tmem + C::kColO + h * D, tmem + h * 128 + kk * 8,
+                           tc::sdesc_mnmajor_sw128(v + kk * 2048, 16384, 1024), id_o,
+                           !first || kk > 0);
+          tc::mma_commit(odone(h));
+        };
+        for (int seg = 0;; ++seg) {
+          const int n = seg_tiles();
+          const bool two = cur.blk.pos1(cur.k) - cur.blk.pos0(cur.k) >= tb2;
+          wait(qfull, seg & 1);
+          wait(kfull(it & 1), (it >> 1) & 1);
+          tc::fence_after_sync();
+          scores(0, it);
+          if (two) scores(1, it);
+          tc::mma_commit(kfree(it & 1));
+          if (n == 1) tc::mma_commit(qfree);
+          for (int i = 0; i < n; ++i, ++it) {
+            wait(vfull(it & 1), (it >> 1) & 1);
+            values(0, it, i == 0);
+            if (i + 1 < n) {
+              wait(kfull((it + 1) & 1), ((it + 1) >> 1) & 1);
+              tc::fence_after_sync();
+              scores(0, it + 1);
+            }
+            if (two) values(1, it, i == 0);
+            tc::mma_commit(vfree(it & 1));
+            if (i + 1 < n) {
+              if (two) scores(1, it + 1);
+              tc::mma_commit(kfree((it + 1) & 1));
+              if (i + 2 == n) tc::mma_commit(qfree);
+            }
+          }
+          left -= n;
+          if (left <= 0 || !cur.next_unit()) break;
+        }
+      }
+      __syncwarp();
+    } else if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+      // ------------------------------------------------ queries and cache tiles
+      constexpr int kCols = D / 16;            // 16-code chunks of a row
+      constexpr int kRows = kConvert / kCols;  // rows of a pass
+      constexpr int kPass = kPageTile / kRows;
+      const int ct = tid - 256, cw = warp - 8;
+      const int col = ct % kCols, row = ct / kCols;
+      // queries: a row's pairs over kLanes lanes, two to a lane
+      constexpr int kLanes = D / 4;
+      const int ql = lane % kLanes;
+      const double turn0 = s.turns[2 * ql], turn1 = s.turns[2 * ql + 1];
+      uint4 kr[kPass], vr[kPass];
+
+      for (int seg = 0;; ++seg) {
+        const int n = seg_tiles();
+        const int t0 = cur.blk.tile0(cur.k) + cur.tile;
+        const int p0 = cur.blk.pos0(cur.k), p1 = cur.blk.pos1(cur.k);
+        const int lo = cur.blk.lo(cur.k);
+        const int all_lo = s.window ? (p1 - p0 < s.window ? max(p1 - s.window + 1, 0) : INT32_MAX) : 0;
+        // lane i: page of tokens 16 (i % 8) .. of a tile, or -1
+        auto look = [&](int i) {
+          const int64_t first = (int64_t)(t0 + i) * kPageTile + (lane & 7) * 16;
+          return i < n && first <= p1 && first + 16 > lo ? page_of(s, cur.b, (int)(first / s.T)) : -1;
+        };
+        auto fetch = [&](const uint8_t* __restrict__ pool, int i, int pg, uint4 (&r)[kPass]) {
+          const int64_t tile0 = (int64_t)(t0 + i) * kPageTile;
+#pragma unroll
+          for (int j = 0; j < kPass; ++j) {
+            const int rr = j * kRows + row;
+            const int p = __shfl_sync(0xffffffffu, pg, rr >> 4);
+            const int64_t tok = tile0 + rr;
+            r[j] = make_uint4(0, 0, 0, 0);
+            if (p >= 0 && tok >= lo && tok <= p1)
+              r[j] = *(const uint4*)(pool + (((size_t)p * s.U + cur.u) * s.T + ((int)tok & (s.T - 1))) * D +
+                                     col * 16);
+          }
+        };
+        // f16 rows into a swizzled tile: blocks of 64 elements (128 bytes) by row
+        auto store = [&](uint32_t tile, int rr, const uint32_t (&x)[8]) {
+          const int c = 2 * col;
+          const uint32_t base = tile + (uint32_t)(c >> 3) * 16384 + rr * 128;
+          const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), bq = make_uint4(x[4], x[5], x[6], x[7]);
+          // the upper columns store their second chunk first: eight lanes then hit all banks
+          const bool flip = col >= 4;
+          const uint32_t o0 = base + (((c & 7) ^ (rr & 7)) << 4), o1 = base + ((((c & 7) + 1) ^ (rr & 7)) << 4);
+          *(uint4*)(smem + (flip ? o1 : o0)) = flip ? bq : a;
+          *(uint4*)(smem + (flip ? o0 : o1)) = flip ? a : bq;
+        };
+        int pg = look(0), pg_next = look(1);
+        float ks = 0.f, vs = 0.f;
+        if (pg >= 0) {
+          ks = k_scales[(size_t)pg * s.U + cur.u];
+          vs = v_scales[(size_t)pg * s.U + cur.u];
+        }
+        fetch(k_pages, 0, pg, kr);
+        fetch(v_pages, 0, pg, vr);
+
+        // ---- queries
+        if (seg > 0) wait(qfree, (seg - 1) & 1);
+        {
+          const int live = (p1 - p0 + 1) * s.G;  // rows
+          const int groups = 4 * (32 / kLanes);
+          const int per = (2 * tb2 * s.G + groups - 1) / groups;
+          const int r0 = (cw * (32 / kLanes) + lane / kLanes) * per;
+          int i = r0 / s.G, g = r0 - i * s.G, had = -1;
+          float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
+          constexpr int kBatch = 8;
+          for (int a0 = 0; a0 < per; a0 += kBatch) {
+            uint32_t xa[kBatch], xb[kBatch];
+            int i2 = i, g2 = g;
+#pragma unroll
+            for (int a = 0; a < kBatch; ++a) {
+              xa[a] = xb[a] = 0;
+              if (a0 + a < per && r0 + a0 + a < live) {
+                const __nv_bfloat16* src = q + (int64_t)(cur.row0 + cur.k * w.tb + i2) * q_stride +
+                                           (cur.u * s.G + g2) * D + 2 * ql;
+                xa[a] = *(const uint32_t*)src;
+                xb[a] = *(const uint32_t*)(src + D / 2);
+              }
+              if (++g2 == s.G) g2 = 0, ++i2;
+            }
+#pragma unroll
+            for (int a = 0; a < kBatch; ++a) {
+              const bool here = a0 + a < per && r0 + a0 + a < live;
+              if (s.rotate && here && i != had) {
+                page_cs(p0 + i, turn0, c0, s0);
+                page_cs(p0 + i, turn1, c1, s1);
+                had = i;
+              }
+              const float a0f = __uint_as_float(xa[a] << 16), a1f = __uint_as_float(xa[a] & 0xFFFF0000u);
+              const float b0f = __uint_as_float(xb[a] << 16), b1f = __uint_as_float(xb[a] & 0xFFFF0000u);
+              const float y0 = a0f * c0 - b0f * s0, y1 = a1f * c1 - b1f * s1;
+              const float z0 = b0f * c0 + a0f * s0, z1 = b1f * c1 + a1f * s1;
+              float am = fmaxf(fmaxf(fabsf(y0), fabsf(y1)), fmaxf(fabsf(z0), fabsf(z1)));
+#pragma unroll
+              for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+              // power of two that brings the row's largest element into [2^7, 2^8)
+              int ex = (int)(__float_as_uint(am) >> 23) - 127 - 7;
+              ex = min(max(ex, -119), 119);
+              const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
+              if (here) {
+                const int h = i >= tb2, r = (i - (h ? tb2 : 0)) * s.G + g;  // row in the half
+                if (ql == 0)
+                  qfac[seg & 1][h * 128 + r] =
+                      s.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex) << 23);
+                unsigned char* dst = smem + h * C::kQHalf + r * 128;
+                const int sw = (r & 7) << 4;
+                *(uint32_t*)(dst + ((4 * ql) ^ sw)) = half2_bits(y0 * mul, y1 * mul);
+                if constexpr (D == 128)
+                  *(uint32_t*)(dst + 16384 + ((4 * ql) ^ sw)) = half2_bits(z0 * mul, z1 * mul);
+                else
+                  *(uint32_t*)(dst + ((4 * ql + 64) ^ sw)) = half2_bits(z0 * mul, z1 * mul);
+              }
+              if (++g == s.G) g = 0, ++i;
+            }
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(qfull);
+
+        // ---- tiles
+        for (int i = 0; i < n; ++i, ++it) {
+          const int st = it & 1;
+          const int64_t tile0 = (int64_t)(t0 + i) * kPageTile;
+          const uint32_t loaded = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+          const bool full = tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu;
+          TileScales& mt = meta[it & (kRing - 1)];
+          // value scale f * 2^e; zeros and what is not finite keep e = 0
+          int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
+          if (e < -100 || e > 100) e = 0;
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          const float vf = vs * down;
+          wait(kfree(st), ((it >> 1) & 1) ^ 1);
+          if (ct < 8) {
+            mt.ks[ct] = fabsf(ks);
+            mt.ve[ct] = (float)e;
+            mt.ive[ct] = down;
+            if (ct == 0) mt.loaded = loaded;
+            // a later tile's; all have left the slot's last one, and none is there yet
+            if (ct < 4) meta[(it + 2) & (kRing - 1)].nan[ct] = 0;
+          }
+          const uint32_t flip = (__float_as_uint(ks) >> 31) * 0x80008000u;
+#pragma unroll
+          for (int j = 0; j < kPass; ++j) {
+            const int rr = j * kRows + row;
+            const uint32_t f = __shfl_sync(0xffffffffu, flip, rr >> 4);
+            uint32_t x[8];
+            widen16(kr[j], x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] ^= f;
+            store(C::kOffK + st * C::kTileBytes, rr, x);
+          }
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(kfull(st));
+          const int pg_next2 = look(i + 2);
+          fetch(k_pages, i + 1, pg_next, kr);
+          float ks_next = 0.f, vs_next = 0.f;
+          if (pg_next >= 0) {
+            ks_next = k_scales[(size_t)pg_next * s.U + cur.u];
+            vs_next = v_scales[(size_t)pg_next * s.U + cur.u];
+          }
+          wait(vfree(st), ((it >> 1) & 1) ^ 1);
+          const __half2 fh = __float2half2_rn(vf);
+          const uint32_t fb = *(const uint32_t*)&fh;
+#pragma unroll
+          for (int j = 0; j < kPass; ++j) {
+            const int rr = j * kRows + row;
+            if (!full) {
+              // Rows differ in what they see.  A NaN would not be hidden by a
+              // weight of zero: such a token's values become zeros, and the NaN is
+              // handed to the rows that see it by their weights.
+              const bool nan = has_nan(vr[j].x) || has_nan(vr[j].y) || has_nan(vr[j].z) || has_nan(vr[j].w);
+              const uint32_t any = __ballot_sync(0xffffffffu, nan);
+              if ((any >> (lane / kCols * kCols)) & ((1u << kCols) - 1u)) {
+                vr[j] = make_uint4(0, 0, 0, 0);
+                if (col == 0) atomicOr(&mt.nan[rr >> 5], 1u << (rr & 31));
+              }
+            }
+            const uint32_t f = __shfl_sync(0xffffffffu, fb, rr >> 4);
+            uint32_t x[8];
+            widen16(vr[j], x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __half2 y = __hmul2(*(const __half2*)&x[k], *(const __half2*)&f);
+              x[k] = *(const uint32_t*)&y;
+            }
+            store(C::kOffV + st * C::kTileBytes, rr, x);
+          }
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(vfull(st));
+          fetch(v_pages, i + 1, pg_next, vr);
+          pg = pg_next;
+          ks = ks_next;
+          vs = vs_next;
+          pg_next = pg_next2;
+        }
+        left -= n;
+        if (left <= 0 || !cur.next_unit()) break;
+      }
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      // ------------------------------------------------ softmax
+      const int h = warp >> 2, r = tid & 127;
+      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t cs = lanes + h * 128, co = lanes + C::kColO + h * D;
+      const int ri = r / s.G, rg = r - ri * s.G;  // token in the half, head in the group
+      int cnt = 0;  // tiles of this half so far
+      int64_t x = x0;
+      for (int seg = 0;; ++seg) {
+        const int n = seg_tiles();
+        const int t0 = cur.blk.tile0(cur.k) + cur.tile;
+        const int p0 = cur.blk.pos0(cur.k), p1 = cur.blk.pos1(cur.k);
+        const int all_lo = s.window ? (p1 - p0 < s.window ? max(p1 - s.window + 1, 0) : INT32_MAX) : 0;
+        const int ti = h * tb2 + ri;  // token in the block
+        const bool live = ri < tb2 && p0 + ti <= p1;
+        const int pos = live ? p0 + ti : -1;
+        const int see_lo = s.window && live ? max(pos - s.window + 1, 0) : 0;
+        if (h == 0 || p1 - p0 >= tb2) {
+          float m = -INFINITY, l = 0.f, fac = 0.f;
+          for (int i = 0; i < n; ++i, ++cnt) {
+            const TileScales& mt = meta[(it + i) & (kRing - 1)];
+            const int64_t tile0 = (int64_t)(t0 + i) * kPageTile;
+            wait(sready(h), cnt & 1);
+            tc::fence_after_sync();
+            if (i == 0) fac = qfac[seg & 1][h * 128 + r];
+            float t[kPageTile];
+#pragma unroll
+            for (int c = 0; c < kPageTile; c += 32) tc::tmem_ld32(cs + c, t + c);
+            // t = S * c + e by group of 16 tokens
+            float c[8], e[8];
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+              const float4 a = *(const float4*)&mt.ks[k], b4 = *(const float4*)&mt.ve[k];
+              c[k] = a.x * fac, c[k + 1] = a.y * fac, c[k + 2] = a.z * fac, c[k + 3] = a.w * fac;
+              e[k] = b4.x, e[k + 1] = b4.y, e[k + 2] = b4.z, e[k + 3] = b4.w;
+            }
+            const uint32_t loaded = mt.loaded;
+            tc::tmem_ld_wait();
+            if (!(tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu)) {
+              const int hi = (int)max(min((int64_t)pos - tile0, (int64_t)kPageTile), (int64_t)-1);
+              const int lo = (int)max(min((int64_t)see_lo - tile0, (int64_t)kPageTile), (int64_t)0);
+              wait(vfull((it + i) & 1), ((it + i) >> 1) & 1);  // the NaN bits
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int top = (loaded >> k) & 1u ? hi : -1;
+                const uint32_t nan = mt.nan[k >> 1] >> (16 * (k & 1));
+#pragma unroll
+                for (int j = 16 * k; j < 16 * k + 16; ++j) {
+                  float y = fmaf(t[j], c[k], e[k]);
+                  if ((nan >> (j & 15)) & 1u) y = __uint_as_float(0x7FC00000u);
+                  t[j] = j <= top && j >= lo ? y : -INFINITY;
+                }
+                c[k] = 1.f;
+                e[k] = 0.f;
+              }
+            }
+            float mt_ = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float a = t[16 * k];
+#pragma unroll
+              for (int j = 1; j < 16; ++j) a = fmaxf(a, t[16 * k + j]);
+              mt_ = fmaxf(mt_, fmaf(a, c[k], e[k]));
+            }
+            const bool grow = mt_ > m + kSlack || (m == -INFINITY && mt_ > m);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float al = grow ? ex2(m - mt_) : 1.f;  // 0 from m = -inf
+              if (grow) m = mt_;
+              l *= al;
+              if (i > 0) {  // the sums so far (of this piece) follow
+                wait(odone(h), (cnt - 1) & 1);
+                tc::fence_after_sync();
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                  uint32_t v[16];
+                  tc::tmem_ld16(co + c0, v);
+                  tc::tmem_ld_wait();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                  tc::tmem_st16(co + c0, v);
+                }
+              }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float d = e[k] - ref;
+              float sum = 0.f;
+#pragma unroll
+              for (int j = 16 * k; j < 16 * k + 16; ++j) {
+                t[j] = ex2(fmaf(t[j], c[k], d));
+                sum += t[j];
+              }
+              l = fmaf(sum, mt.ive[k], l);
+              if (k & 1) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  pk[j] = half2_bits(t[16 * (k - 1) + 2 * j], t[16 * (k - 1) + 2 * j + 1]);
+                tc::tmem_st16(cs + 8 * (k - 1), pk);
+              }
+            }
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            tc::mbar_arrive(pready(h));
+          }
+
+          // ---- the piece's result
+          wait(odone(h), (cnt - 1) & 1);
+          tc::fence_after_sync();
+          const bool whole = cur.tile == 0 && n == cur.tiles;
+          const int slot = 2 * blockIdx.x + (cur.tile == 0 ? 1 : 0);
+          const size_t prow = (size_t)slot * w.rows + ti * s.G + rg;
+          const int64_t orow = (int64_t)(cur.row0 + cur.k * w.tb + ti) * s.Hq + cur.u * s.G + rg;
+          if (live && !whole) w.ml[prow] = make_float2(m, l);
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float v[32];
+            tc::tmem_ld32(co + c0, v);
+            tc::tmem_ld_wait();
+            if (live) {
+              if (whole) {
+                uint4* dst = (uint4*)(out + orow * D + c0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t y[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    float a = v[8 * k + 2 * j] * inv, b2 = v[8 * k + 2 * j + 1] * inv;
+                    if (l == 0.f) a = b2 = 0.f;
+                    const __nv_bfloat162 hb = __floats2bfloat162_rn(a, b2);
+                    y[j] = *(const uint32_t*)&hb;
+                  }
+                  dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+              } else {
+                float4* dst = (float4*)(w.acc + prow * D + c0);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              }
+            }
+          }
+          tc::fence_before_sync();
+        }
+        if (tid == 0 && cur.tile == 0 && n < cur.tiles)
+          w.info[blockIdx.x] = make_int4(cur.row0 + cur.k * w.tb, cur.u, (p1 - p0 + 1) * s.G,
+                                         (int)share_of_tile(x + cur.tiles - 1, total, gridDim.x));
+        it += n;
+        left -= n;
+        x += n;
+        if (left <= 0 || !cur.next_unit()) break;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 12) tc::tmem_dealloc(tmem, C::kTmem);
+}
+
+template <int D>
+cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
+                   const void* kp, const void* vp, const float* ks, const float* vs, void* out,
+                   cudaStream_t stream) {
+  static int done[kMaxDevices];
+  auto kern = page_many_kernel<D>;
+  const cudaError_t e = ensure_smem(kern, Many<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(kPageGrid), dim3(kThreads), Many<D>::kSmem, stream, true, s, w,
+                  (const __nv_bfloat16*)q, q_stride, (const uint8_t*)kp, (const uint8_t*)vp, ks, vs,
+                  (__nv_bfloat16*)out);
+}
+
+}  // namespace
+
+cudaError_t launch_page_many(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
+                             const void* k_pages, const void* v_pages, const float* k_scales,
+                             const float* v_scales, void* out, cudaStream_t stream) {
+  return s.d == 64 ? launch<64>(s, w, q, q_stride, k_pages, v_pages, k_scales, v_scales, out, stream)
+                   : launch<128>(s, w, q, q_stride, k_pages, v_pages, k_scales, v_scales, out, stream);
+}
+
+}  // namespace salsc

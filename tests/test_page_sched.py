@@ -1,6 +1,6 @@
 """The paged attention's work list (csrc/page_sched.cuh), compiled from the library's own header
-for the host and checked against counting the tiles one by one: tiles of a row block, tiles before
-a row block, and the row block that holds a tile."""
+for the host and checked against counting the tiles one by one: tiles of a row block and tiles before
+a row block."""
 import os
 import shutil
 import subprocess
@@ -40,22 +40,19 @@ int main() {
       } else {
         if (p.tile0(k) != first || p.tiles(k) != last - first + 1) return 4;
       }
-      for (int t = 0; t < p.tiles(k); t += 1 + (int)rnd(9))
-        if (p.block_of(before + t) != k) return 5;
-      if (p.block_of(before + p.tiles(k) - 1) != k) return 6;
       before += p.tiles(k);
     }
-    if (p.before(p.count()) != before) return 7;
+    if (p.before(p.count()) != before) return 5;
   }
   // the largest sizes: no 32-bit overflow
   const PageBlocks big{2147483647, 2147483647, 8, 0};
-  if (big.tiles(big.count() - 1) != 16777216) return 8;
+  if (big.tiles(big.count() - 1) != 16777216) return 6;
   long long full = 0;
   for (long long k = 0; k < big.count(); ++k) {
     const long long e = (k + 1) * 8 < 2147483647ll ? (k + 1) * 8 : 2147483647ll;
     full += (e - 1) / 128 + 1;
   }
-  if (big.before(big.count()) != full) return 9;
+  if (big.before(big.count()) != full) return 7;
   std::printf("ok\n");
   return 0;
 }
