@@ -34,7 +34,7 @@ constexpr int kConvert = 128;   // threads of the converting warps
 constexpr int kRing = 8;        // tiles' scales that are kept
 constexpr float kSlack = 8.f;   // log2 units
 
-struct TileScales {
+struct alignas(16) TileScales {  // read by float4
   float ks[8], ve[8], ive[8];  // by group of 16 tokens: |key scale|, e, 2^-e
   uint32_t loaded;             // groups that were loaded (bits)
   uint32_t nan[4];             // tokens whose values hold a NaN, where rows differ in what they see

@@ -139,6 +139,13 @@ def test_attend_one_long_sequence(dtype):
     check_attend(Step([9001], [70], 4, 1, 128, 128, dtype, seed=6))
 
 
+@pytest.mark.parametrize("lens,news,hq,hkv,d,page,window", [
+    ([1700], [1700], 8, 4, 128, 64, 0), ([1300, 900, 5], [1300, 333, 1], 6, 6, 128, 16, 0),
+    ([2100], [1500], 8, 4, 64, 32, 0), ([2500, 700], [1000, 700], 16, 4, 128, 128, 300)])
+def test_attend_prompt_of_several_units_and_tiles_a_cta(lens, news, hq, hkv, d, page, window):
+    check_attend(Step(lens, news, hq, hkv, d, page, window=window, seed=8, page_gain=1.0))
+
+
 @pytest.mark.parametrize("window", [1, 2, 17, 100, 128, 129, 400])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attend_window(window, dtype):
