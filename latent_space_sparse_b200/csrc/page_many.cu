@@ -22,7 +22,7 @@
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of a half (a
 // thread per row), warps 8-11 queries (rotation, f16) and cache tiles (codes
-// to f16, global to shared memory), warp 12 issues the MMAs.
+// to f16), warp 12 issues the MMAs, warp 13 copies pages to shared memory.
 #include "page.cuh"
 #include "tc.cuh"
 
@@ -31,13 +31,38 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kConvert = 128;   // threads of the converting warps
-constexpr int kRing = 8;        // tiles' scales that are kept
+constexpr int kRing = 4;        // tiles whose scales are kept
 constexpr float kSlack = 8.f;   // log2 units
 
+// What the copying warp says of a tile, by group of 16 tokens.
 struct alignas(16) TileScales {  // read by float4
-  float ks[8], ve[8], ive[8];  // by group of 16 tokens: |key scale|, e, 2^-e
-  uint32_t loaded;             // groups that were loaded (bits)
-  uint32_t nan[4];             // tokens whose values hold a NaN, where rows differ in what they see
+  float ks[8], ve[8], ive[8];  // key scale; value scale f * 2^e: e, 2^-e
+  uint32_t vf[8];              // f, twice in f16
+  uint32_t loaded, pad[3];     // groups that were loaded (bits)
+};
+
+// A segment: a piece of one unit, this CTA's tiles of it.  Warp 13 writes them.
+struct alignas(16) Segment {
+  int n, t0;    // tiles (0: there are no more segments), first tile
+  int p0, p1;   // positions of the unit's first and last row
+  int lo;       // first token that any row sees
+  int all_lo;   // first token that no row sees too late (window)
+  int row;      // token row of the first row
+  short u;      // KV head
+  bool starts, whole;  // the unit's first tile is in the segment; all of them are
+};
+// A segment's entry is read until its last tile's results are out; the copying warp is at most
+// four tiles ahead of that.
+constexpr int kSegments = 8;
+
+struct Shared {
+  int8_t qexp[2][256];  // by segment parity: exponent of the row's power of two
+  Segment segments[kSegments];
+  TileScales meta[kRing];
+  uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
+  uint64_t bars[20 + kSegments];
+  int64_t share[kThreads / 32 + 2];
+  uint32_t tmem_base;
 };
 
 template <int D>
@@ -46,7 +71,11 @@ struct Many {
   static constexpr int kTileBytes = kPageTile * D * 2;
   static constexpr int kOffK = 2 * kQHalf;
   static constexpr int kOffV = kOffK + 2 * kTileBytes;
-  static constexpr int kSmem = kOffV + 2 * kTileBytes + 1024;  // + alignment
+  static constexpr int kOffCodes = kOffV + 2 * kTileBytes;  // of K, then of V
+  static constexpr int kCodeBytes = kPageTile * D;
+  static constexpr int kOffShared = kOffCodes + 2 * kCodeBytes;
+  static constexpr int kSmem = kOffShared + (int)sizeof(Shared);
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static constexpr int kTmem = 512;
   static constexpr int kColO = 256;
 };
@@ -87,17 +116,13 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
                  const float* __restrict__ k_scales, const float* __restrict__ v_scales,
                  __nv_bfloat16* __restrict__ out) {
   using C = Many<D>;
-  extern __shared__ unsigned char smem_raw[];
-  __shared__ TileScales meta[kRing];
-  __shared__ alignas(8) uint64_t bars[16];
-  __shared__ int64_t share[kThreads / 32 + 2];
-  __shared__ float qfac[2][256];  // by segment parity: softmax scale * log2(e) / the row's power of two
-  __shared__ uint32_t tmem_base;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared& sh = *(Shared*)(smem + C::kOffShared);
+  auto& meta = sh.meta;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t sm0 = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  unsigned char* smem = smem_raw + (sm0 - tc::smem_u32(smem_raw));
-  const uint32_t bar0 = tc::smem_u32(bars);
+  const uint32_t sm0 = tc::smem_u32(smem);
+  const uint32_t bar0 = tc::smem_u32(sh.bars);
   auto kfull = [&](int i) { return bar0 + 8u * i; };
   auto kfree = [&](int i) { return bar0 + 8u * (2 + i); };
   auto vfull = [&](int i) { return bar0 + 8u * (4 + i); };
@@ -106,6 +131,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   auto pready = [&](int h) { return bar0 + 8u * (10 + h); };
   auto odone = [&](int h) { return bar0 + 8u * (12 + h); };
   const uint32_t qfull = bar0 + 8u * 14, qfree = bar0 + 8u * 15;
+  auto cfull = [&](int v) { return bar0 + 8u * (16 + v); };  // codes of K, of V
+  auto cfree = [&](int v) { return bar0 + 8u * (18 + v); };
+  auto segfull = [&](int i) { return bar0 + 8u * (20 + i % kSegments); };
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -116,23 +144,26 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       tc::mbar_init(sready(i), 2);  // the scores, and the issuer for what it has waited for
       tc::mbar_init(pready(i), 128);
       tc::mbar_init(odone(i), 1);
+      tc::mbar_init(cfull(i), 1);
+      tc::mbar_init(cfree(i), kConvert);
     }
     tc::mbar_init(qfull, kConvert);
     tc::mbar_init(qfree, 1);
+    for (int i = 0; i < kSegments; ++i) tc::mbar_init(segfull(i), 1);
     tc::mbar_fence_init();
   }
-  if (warp == 12) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
-  if (tid < kRing * 4) meta[tid / 4].nan[tid % 4] = 0;
+  if (warp == 12) tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), C::kTmem);
+  if (tid < 2 * kRing * 4) sh.nan[tid / 4][tid % 4] = 0;
   grid_dependency_wait();
   allow_dependent_launch();
   int64_t total, x0, x1, rem;
   int b;
-  page_share(s, w, share, total, x0, x1, b, rem);
+  page_share(s, w, sh.share, total, x0, x1, b, rem);
   if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = sh.tmem_base;
   bool dead = false;  // a wait gave up: skip the others, so that the kernel ends
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (!dead && !tc::mbar_wait(bar, parity, s.flags)) dead = true;
@@ -140,13 +171,12 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   const int tb2 = w.tb / 2;  // new tokens of a half
 
   if (x0 < x1) {
-    PageCursor cur(s, w);
-    page_seek(cur, b, rem);
-    int64_t left = x1 - x0;
     int it = 0;  // tiles so far
-    // tiles of the current segment; a segment is a piece of one unit
-    auto seg_tiles = [&] { return (int)min((int64_t)(cur.tiles - cur.tile), left); };
-    // 184 * 256 + 104 * 128 + 40 * 128 = 128 * 512 registers
+    auto segment = [&](int i) -> const Segment& {
+      wait(segfull(i), (i / kSegments) & 1);
+      return sh.segments[i % kSegments];
+    };
+    // 200 * 256 + 72 * 128 + 40 * 128 = 128 * 512 registers
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
       // ------------------------------------------------ MMA issuer
@@ -154,32 +184,39 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, kPageTile, false);
         constexpr uint32_t id_o = tc::idesc_f16_f32(128, D, true);
         int cnt[2] = {0, 0};
+        // descriptors are formed from opaque starts, so that the compiler does not
+        // keep one for every step in registers
+        auto opaque = [](uint64_t d) {
+          asm volatile("" : "+l"(d));
+          return d;
+        };
         auto scores = [&](int h, int i) {
-          const uint32_t k = sm0 + C::kOffK + (uint32_t)(i & 1) * C::kTileBytes;
-          const uint32_t qa = sm0 + (uint32_t)h * C::kQHalf;
+          const uint64_t qa = opaque(tc::sdesc_kmajor_sw128(sm0 + (uint32_t)h * C::kQHalf));
+          const uint64_t ka = opaque(tc::sdesc_kmajor_sw128(sm0 + C::kOffK + (uint32_t)(i & 1) * C::kTileBytes));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)(kk / 4) * 16384 + (kk % 4) * 32;
-            tc::mma_bf16(tmem + h * 128, tc::sdesc_kmajor_sw128(qa + off),
-                         tc::sdesc_kmajor_sw128(k + off), id_s, kk > 0);
+            const uint64_t off = (uint64_t)((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+            tc::mma_bf16(tmem + h * 128, qa + off, ka + off, id_s, kk > 0);
           }
           tc::mma_commit(sready(h));
           tc::mbar_arrive(sready(h));
         };
         auto values = [&](int h, int i, bool first) {
-          const uint32_t v = sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes;
+          const uint64_t va =
+              opaque(tc::sdesc_mnmajor_sw128(sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes, 16384, 1024));
           wait(pready(h), cnt[h]++ & 1);
           tc::fence_after_sync();
 #pragma unroll
           for (int kk = 0; kk < kPageTile / 16; ++kk)
-            tc::mma_f16_ts(tmem + C::kColO + h * D, tmem + h * 128 + kk * 8,
-                           tc::sdesc_mnmajor_sw128(v + kk * 2048, 16384, 1024), id_o,
+            tc::mma_f16_ts(tmem + C::kColO + h * D, tmem + h * 128 + kk * 8, va + (kk * 2048 >> 4), id_o,
                            !first || kk > 0);
           tc::mma_commit(odone(h));
         };
         for (int seg = 0;; ++seg) {
-          const int n = seg_tiles();
-          const bool two = cur.blk.pos1(cur.k) - cur.blk.pos0(cur.k) >= tb2;
+          const Segment& sg = segment(seg);
+          const int n = dead ? 0 : sg.n;
+          if (n == 0) break;
+          const bool two = sg.p1 - sg.p0 >= tb2;
           wait(qfull, seg & 1);
           wait(kfull(it & 1), (it >> 1) & 1);
           tc::fence_after_sync();
@@ -203,13 +240,94 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               if (i + 2 == n) tc::mma_commit(qfree);
             }
           }
-          left -= n;
-          if (left <= 0 || !cur.next_unit()) break;
+        }
+      }
+      // ------------------------------------------------ pages to shared memory
+      if (warp == 13) {
+        PageCursor cur(s, w);
+        page_seek(cur, b, rem);
+        int64_t x = x0;
+        for (int seg = 0;; ++seg) {
+          const int n = (int)min((int64_t)(cur.tiles - cur.tile), x1 - x);
+          const int t0 = cur.blk.tile0(cur.k) + cur.tile;
+          const int p0 = cur.blk.pos0(cur.k), hi = cur.blk.pos1(cur.k), lo = cur.blk.lo(cur.k);
+          if (lane == 0) {
+            Segment& sg = sh.segments[seg % kSegments];
+            sg.n = n, sg.t0 = t0, sg.p0 = p0, sg.p1 = hi, sg.lo = lo;
+            sg.all_lo = s.window ? (hi - p0 < s.window ? max(hi - s.window + 1, 0) : INT32_MAX) : 0;
+            sg.row = cur.row0 + cur.k * w.tb;
+            sg.u = (short)cur.u;
+            sg.starts = cur.tile == 0;
+            sg.whole = cur.tile == 0 && n == cur.tiles;
+            tc::mbar_arrive(segfull(seg));
+            if (cur.tile == 0 && n < cur.tiles)  // others go on with the unit
+              w.info[blockIdx.x] = make_int4(cur.row0 + cur.k * w.tb, cur.u, (hi - p0 + 1) * s.G,
+                                             (int)share_of_tile(x + cur.tiles - 1, total, gridDim.x));
+          }
+          x += n;
+          // lane i: the page that holds group i % 8 of a tile, or -1; a page is copied
+          // whole if a row sees any of it
+          auto look = [&](int i) {
+            const int64_t first = (int64_t)(t0 + i) * kPageTile + ((lane & 7) * 16 & -s.T);
+            return i < n && first <= hi && first + s.T > lo ? page_of(s, cur.b, (int)(first / s.T)) : -1;
+          };
+          int pg = look(0);
+          float ks = 0.f, vs = 0.f;
+          auto scales = [&] {
+            ks = vs = 0.f;
+            if (pg >= 0) {
+              ks = k_scales[(size_t)pg * s.U + cur.u];
+              vs = v_scales[(size_t)pg * s.U + cur.u];
+            }
+          };
+          scales();
+          for (int i = 0; i < n; ++i, ++it) {
+            const int pg_next = look(i + 1);
+            const uint32_t loaded = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+            const uint32_t bytes = dead ? 0u : (uint32_t)__popc(loaded) * 16 * D;
+            // a page's first group copies it (a tile holds whole pages)
+            const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
+            const size_t src = (((size_t)max(pg, 0) * s.U + cur.u) * s.T) * D;
+            const uint32_t dst = sm0 + C::kOffCodes + lane * 16 * D;
+            wait(cfree(0), (it & 1) ^ 1);
+            if (lane < 8) {
+              TileScales& mt = meta[it & (kRing - 1)];
+              // zeros and what is not finite keep e = 0
+              int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
+              if (e < -100 || e > 100) e = 0;
+              const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+              mt.ks[lane] = ks;
+              mt.ve[lane] = (float)e;
+              mt.ive[lane] = down;
+              mt.vf[lane] = half2_bits(vs * down, vs * down);
+              if (lane == 0) mt.loaded = loaded;
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_expect_tx(cfull(0), bytes);
+            __syncwarp();
+            if (first && !dead) tc::bulk_load(dst, k_pages + src, (uint32_t)(s.T * D), cfull(0));
+            wait(cfree(1), (it & 1) ^ 1);
+            __syncwarp();
+            const uint32_t vbytes = __any_sync(0xffffffffu, dead) ? 0u : bytes;
+            if (lane == 0) tc::mbar_expect_tx(cfull(1), vbytes);
+            __syncwarp();
+            if (first && vbytes)
+              tc::bulk_load(dst + C::kCodeBytes, v_pages + src, (uint32_t)(s.T * D), cfull(1));
+            pg = pg_next;
+            scales();
+          }
+          if (x >= x1 || !cur.next_unit()) {
+            if (lane == 0) {
+              sh.segments[(seg + 1) % kSegments].n = 0;
+              tc::mbar_arrive(segfull(seg + 1));
+            }
+            break;
+          }
         }
       }
       __syncwarp();
     } else if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       // ------------------------------------------------ queries and cache tiles
       constexpr int kCols = D / 16;            // 16-code chunks of a row
       constexpr int kRows = kConvert / kCols;  // rows of a pass
@@ -220,32 +338,13 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       constexpr int kLanes = D / 4;
       const int ql = lane % kLanes;
       const double turn0 = s.turns[2 * ql], turn1 = s.turns[2 * ql + 1];
-      uint4 kr[kPass], vr[kPass];
 
       for (int seg = 0;; ++seg) {
-        const int n = seg_tiles();
-        const int t0 = cur.blk.tile0(cur.k) + cur.tile;
-        const int p0 = cur.blk.pos0(cur.k), p1 = cur.blk.pos1(cur.k);
-        const int lo = cur.blk.lo(cur.k);
-        const int all_lo = s.window ? (p1 - p0 < s.window ? max(p1 - s.window + 1, 0) : INT32_MAX) : 0;
-        // lane i: page of tokens 16 (i % 8) .. of a tile, or -1
-        auto look = [&](int i) {
-          const int64_t first = (int64_t)(t0 + i) * kPageTile + (lane & 7) * 16;
-          return i < n && first <= p1 && first + 16 > lo ? page_of(s, cur.b, (int)(first / s.T)) : -1;
-        };
-        auto fetch = [&](const uint8_t* __restrict__ pool, int i, int pg, uint4 (&r)[kPass]) {
-          const int64_t tile0 = (int64_t)(t0 + i) * kPageTile;
-#pragma unroll
-          for (int j = 0; j < kPass; ++j) {
-            const int rr = j * kRows + row;
-            const int p = __shfl_sync(0xffffffffu, pg, rr >> 4);
-            const int64_t tok = tile0 + rr;
-            r[j] = make_uint4(0, 0, 0, 0);
-            if (p >= 0 && tok >= lo && tok <= p1)
-              r[j] = *(const uint4*)(pool + (((size_t)p * s.U + cur.u) * s.T + ((int)tok & (s.T - 1))) * D +
-                                     col * 16);
-          }
-        };
+        const Segment& sg = segment(seg);
+        const int n = dead ? 0 : sg.n;
+        if (n == 0) break;
+        const int p0 = sg.p0, p1 = sg.p1, lo = sg.lo, all_lo = sg.all_lo;
+        const int64_t first = (int64_t)sg.t0 * kPageTile;
         // f16 rows into a swizzled tile: blocks of 64 elements (128 bytes) by row
         auto store = [&](uint32_t tile, int rr, const uint32_t (&x)[8]) {
           const int c = 2 * col;
@@ -257,15 +356,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           *(uint4*)(smem + (flip ? o1 : o0)) = flip ? bq : a;
           *(uint4*)(smem + (flip ? o0 : o1)) = flip ? a : bq;
         };
-        int pg = look(0), pg_next = look(1);
-        float ks = 0.f, vs = 0.f;
-        if (pg >= 0) {
-          ks = k_scales[(size_t)pg * s.U + cur.u];
-          vs = v_scales[(size_t)pg * s.U + cur.u];
-        }
-        fetch(k_pages, 0, pg, kr);
-        fetch(v_pages, 0, pg, vr);
-
         // ---- queries
         if (seg > 0) wait(qfree, (seg - 1) & 1);
         {
@@ -283,8 +373,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             for (int a = 0; a < kBatch; ++a) {
               xa[a] = xb[a] = 0;
               if (a0 + a < per && r0 + a0 + a < live) {
-                const __nv_bfloat16* src = q + (int64_t)(cur.row0 + cur.k * w.tb + i2) * q_stride +
-                                           (cur.u * s.G + g2) * D + 2 * ql;
+                const __nv_bfloat16* src = q + (int64_t)(sg.row + i2) * q_stride + (sg.u * s.G + g2) * D + 2 * ql;
                 xa[a] = *(const uint32_t*)src;
                 xb[a] = *(const uint32_t*)(src + D / 2);
               }
@@ -311,9 +400,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
               if (here) {
                 const int h = i >= tb2, r = (i - (h ? tb2 : 0)) * s.G + g;  // row in the half
-                if (ql == 0)
-                  qfac[seg & 1][h * 128 + r] =
-                      s.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex) << 23);
+                if (ql == 0) sh.qexp[seg & 1][h * 128 + r] = (int8_t)ex;
                 unsigned char* dst = smem + h * C::kQHalf + r * 128;
                 const int sw = (r & 7) << 4;
                 *(uint32_t*)(dst + ((4 * ql) ^ sw)) = half2_bits(y0 * mul, y1 * mul);
@@ -332,64 +419,56 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         // ---- tiles
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it & 1;
-          const int64_t tile0 = (int64_t)(t0 + i) * kPageTile;
-          const uint32_t loaded = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+          const int64_t tile0 = first + (int64_t)i * kPageTile;
+          const TileScales& mt = meta[it & (kRing - 1)];
+          uint32_t(&nan)[4] = sh.nan[it & (2 * kRing - 1)];
+          wait(cfull(0), it & 1);
+          const uint32_t loaded = mt.loaded;
           const bool full = tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu;
-          TileScales& mt = meta[it & (kRing - 1)];
-          // value scale f * 2^e; zeros and what is not finite keep e = 0
-          int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
-          if (e < -100 || e > 100) e = 0;
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          const float vf = vs * down;
+          // codes of pass j; zeros for tokens that no row sees
+          auto codes = [&](int v, int j) {
+            const int rr = j * kRows + row;
+            const int64_t tok = tile0 + rr;
+            uint4 c = *(const uint4*)(smem + C::kOffCodes + v * C::kCodeBytes + rr * D + col * 16);
+            if (!full && (tok < lo || tok > p1 || !((loaded >> (rr >> 4)) & 1u))) c = make_uint4(0, 0, 0, 0);
+            return c;
+          };
           wait(kfree(st), ((it >> 1) & 1) ^ 1);
-          if (ct < 8) {
-            mt.ks[ct] = fabsf(ks);
-            mt.ve[ct] = (float)e;
-            mt.ive[ct] = down;
-            if (ct == 0) mt.loaded = loaded;
-            // a later tile's; all have left the slot's last one, and none is there yet
-            if (ct < 4) meta[(it + 2) & (kRing - 1)].nan[ct] = 0;
-          }
-          const uint32_t flip = (__float_as_uint(ks) >> 31) * 0x80008000u;
+          // a later tile's; all have left the slot's last one, and none is there yet
+          if (ct < 4) sh.nan[(it + 2) & (2 * kRing - 1)][ct] = 0;
 #pragma unroll
           for (int j = 0; j < kPass; ++j) {
             const int rr = j * kRows + row;
-            const uint32_t f = __shfl_sync(0xffffffffu, flip, rr >> 4);
+            const uint32_t f = (__float_as_uint(mt.ks[rr >> 4]) >> 31) * 0x80008000u;  // its sign
             uint32_t x[8];
-            widen16(kr[j], x);
+            widen16(codes(0, j), x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] ^= f;
             store(C::kOffK + st * C::kTileBytes, rr, x);
           }
           tc::fence_proxy_async_smem();
+          tc::mbar_arrive(cfree(0));
           tc::mbar_arrive(kfull(st));
-          const int pg_next2 = look(i + 2);
-          fetch(k_pages, i + 1, pg_next, kr);
-          float ks_next = 0.f, vs_next = 0.f;
-          if (pg_next >= 0) {
-            ks_next = k_scales[(size_t)pg_next * s.U + cur.u];
-            vs_next = v_scales[(size_t)pg_next * s.U + cur.u];
-          }
+          wait(cfull(1), it & 1);
           wait(vfree(st), ((it >> 1) & 1) ^ 1);
-          const __half2 fh = __float2half2_rn(vf);
-          const uint32_t fb = *(const uint32_t*)&fh;
 #pragma unroll
           for (int j = 0; j < kPass; ++j) {
             const int rr = j * kRows + row;
+            uint4 c = codes(1, j);
             if (!full) {
               // Rows differ in what they see.  A NaN would not be hidden by a
               // weight of zero: such a token's values become zeros, and the NaN is
               // handed to the rows that see it by their weights.
-              const bool nan = has_nan(vr[j].x) || has_nan(vr[j].y) || has_nan(vr[j].z) || has_nan(vr[j].w);
-              const uint32_t any = __ballot_sync(0xffffffffu, nan);
+              const bool bad = has_nan(c.x) || has_nan(c.y) || has_nan(c.z) || has_nan(c.w);
+              const uint32_t any = __ballot_sync(0xffffffffu, bad);
               if ((any >> (lane / kCols * kCols)) & ((1u << kCols) - 1u)) {
-                vr[j] = make_uint4(0, 0, 0, 0);
-                if (col == 0) atomicOr(&mt.nan[rr >> 5], 1u << (rr & 31));
+                c = make_uint4(0, 0, 0, 0);
+                if (col == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
               }
             }
-            const uint32_t f = __shfl_sync(0xffffffffu, fb, rr >> 4);
+            const uint32_t f = mt.vf[rr >> 4];
             uint32_t x[8];
-            widen16(vr[j], x);
+            widen16(c, x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const __half2 y = __hmul2(*(const __half2*)&x[k], *(const __half2*)&f);
@@ -398,30 +477,23 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             store(C::kOffV + st * C::kTileBytes, rr, x);
           }
           tc::fence_proxy_async_smem();
+          tc::mbar_arrive(cfree(1));
           tc::mbar_arrive(vfull(st));
-          fetch(v_pages, i + 1, pg_next, vr);
-          pg = pg_next;
-          ks = ks_next;
-          vs = vs_next;
-          pg_next = pg_next2;
         }
-        left -= n;
-        if (left <= 0 || !cur.next_unit()) break;
       }
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
       // ------------------------------------------------ softmax
       const int h = warp >> 2, r = tid & 127;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t cs = lanes + h * 128, co = lanes + C::kColO + h * D;
       const int ri = r / s.G, rg = r - ri * s.G;  // token in the half, head in the group
       int cnt = 0;  // tiles of this half so far
-      int64_t x = x0;
       for (int seg = 0;; ++seg) {
-        const int n = seg_tiles();
-        const int t0 = cur.blk.tile0(cur.k) + cur.tile;
-        const int p0 = cur.blk.pos0(cur.k), p1 = cur.blk.pos1(cur.k);
-        const int all_lo = s.window ? (p1 - p0 < s.window ? max(p1 - s.window + 1, 0) : INT32_MAX) : 0;
+        const Segment& sg = segment(seg);
+        const int n = dead ? 0 : sg.n;
+        if (n == 0) break;
+        const int p0 = sg.p0, p1 = sg.p1;
         const int ti = h * tb2 + ri;  // token in the block
         const bool live = ri < tb2 && p0 + ti <= p1;
         const int pos = live ? p0 + ti : -1;
@@ -430,39 +502,34 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           float m = -INFINITY, l = 0.f, fac = 0.f;
           for (int i = 0; i < n; ++i, ++cnt) {
             const TileScales& mt = meta[(it + i) & (kRing - 1)];
-            const int64_t tile0 = (int64_t)(t0 + i) * kPageTile;
+            const int64_t tile0 = (int64_t)(sg.t0 + i) * kPageTile;
             wait(sready(h), cnt & 1);
             tc::fence_after_sync();
-            if (i == 0) fac = qfac[seg & 1][h * 128 + r];
+            if (i == 0)
+              fac = s.scale * 1.4426950408889634f *
+                    __uint_as_float((uint32_t)(127 + sh.qexp[seg & 1][h * 128 + r]) << 23);
             float t[kPageTile];
 #pragma unroll
             for (int c = 0; c < kPageTile; c += 32) tc::tmem_ld32(cs + c, t + c);
-            // t = S * c + e by group of 16 tokens
-            float c[8], e[8];
-#pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-              const float4 a = *(const float4*)&mt.ks[k], b4 = *(const float4*)&mt.ve[k];
-              c[k] = a.x * fac, c[k + 1] = a.y * fac, c[k + 2] = a.z * fac, c[k + 3] = a.w * fac;
-              e[k] = b4.x, e[k + 1] = b4.y, e[k + 2] = b4.z, e[k + 3] = b4.w;
-            }
             const uint32_t loaded = mt.loaded;
             tc::tmem_ld_wait();
-            if (!(tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu)) {
+            // t = S * c + e by group of 16 tokens, but where tokens are masked: t itself
+            const bool masked = !(tile0 >= sg.all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu);
+            if (masked) {
               const int hi = (int)max(min((int64_t)pos - tile0, (int64_t)kPageTile), (int64_t)-1);
               const int lo = (int)max(min((int64_t)see_lo - tile0, (int64_t)kPageTile), (int64_t)0);
               wait(vfull((it + i) & 1), ((it + i) >> 1) & 1);  // the NaN bits
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
+                const float c = fabsf(mt.ks[k]) * fac, e = mt.ve[k];
                 const int top = (loaded >> k) & 1u ? hi : -1;
-                const uint32_t nan = mt.nan[k >> 1] >> (16 * (k & 1));
+                const uint32_t nan = sh.nan[(it + i) & (2 * kRing - 1)][k >> 1] >> (16 * (k & 1));
 #pragma unroll
                 for (int j = 16 * k; j < 16 * k + 16; ++j) {
-                  float y = fmaf(t[j], c[k], e[k]);
+                  float y = fmaf(t[j], c, e);
                   if ((nan >> (j & 15)) & 1u) y = __uint_as_float(0x7FC00000u);
                   t[j] = j <= top && j >= lo ? y : -INFINITY;
                 }
-                c[k] = 1.f;
-                e[k] = 0.f;
               }
             }
             float mt_ = -INFINITY;
@@ -471,7 +538,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               float a = t[16 * k];
 #pragma unroll
               for (int j = 1; j < 16; ++j) a = fmaxf(a, t[16 * k + j]);
-              mt_ = fmaxf(mt_, fmaf(a, c[k], e[k]));
+              mt_ = fmaxf(mt_, masked ? a : fmaf(a, fabsf(mt.ks[k]) * fac, mt.ve[k]));
             }
             const bool grow = mt_ > m + kSlack || (m == -INFINITY && mt_ > m);
             if (__any_sync(0xffffffffu, grow)) {
@@ -495,11 +562,11 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float d = e[k] - ref;
+              const float c = masked ? 1.f : fabsf(mt.ks[k]) * fac, d = (masked ? 0.f : mt.ve[k]) - ref;
               float sum = 0.f;
 #pragma unroll
               for (int j = 16 * k; j < 16 * k + 16; ++j) {
-                t[j] = ex2(fmaf(t[j], c[k], d));
+                t[j] = ex2(fmaf(t[j], c, d));
                 sum += t[j];
               }
               l = fmaf(sum, mt.ive[k], l);
@@ -519,10 +586,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           // ---- the piece's result
           wait(odone(h), (cnt - 1) & 1);
           tc::fence_after_sync();
-          const bool whole = cur.tile == 0 && n == cur.tiles;
-          const int slot = 2 * blockIdx.x + (cur.tile == 0 ? 1 : 0);
+          const bool whole = sg.whole;
+          const int slot = 2 * blockIdx.x + (sg.starts ? 1 : 0);
           const size_t prow = (size_t)slot * w.rows + ti * s.G + rg;
-          const int64_t orow = (int64_t)(cur.row0 + cur.k * w.tb + ti) * s.Hq + cur.u * s.G + rg;
+          const int64_t orow = (int64_t)(sg.row + ti) * s.Hq + sg.u * s.G + rg;
           if (live && !whole) w.ml[prow] = make_float2(m, l);
           const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -555,13 +622,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           }
           tc::fence_before_sync();
         }
-        if (tid == 0 && cur.tile == 0 && n < cur.tiles)
-          w.info[blockIdx.x] = make_int4(cur.row0 + cur.k * w.tb, cur.u, (p1 - p0 + 1) * s.G,
-                                         (int)share_of_tile(x + cur.tiles - 1, total, gridDim.x));
         it += n;
-        left -= n;
-        x += n;
-        if (left <= 0 || !cur.next_unit()) break;
       }
     }
   }
