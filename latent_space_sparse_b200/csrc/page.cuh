@@ -134,6 +134,8 @@ struct PageWork {
   float* acc;     // [2 * grid][rows][d] unnormalised outputs
   float2* ml;     // [2 * grid][rows] running maximum (log2 units) and normaliser
   int4* info;     // [grid] of slot 2c + 1: first row's token row, KV head, rows, last CTA of the unit
+  void* qrot;     // many rows only: rotated queries and their rows' exponents (page_many.cu)
+  int8_t* qexp;
 };
 
 // A cursor over the step's units and tiles, for one warp or thread (every

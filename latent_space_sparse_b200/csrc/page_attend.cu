@@ -101,6 +101,10 @@ Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
   if (p.has_many) {
     p.many = layout(s, kPageManyRows, part, p.bytes);
     p.many.tb = 2 * (kPageManyRows / 2 / s.G);
+    p.many.qrot = (char*)part + p.bytes;
+    p.bytes = align_up(p.bytes + (size_t)s.n_tokens * s.Hq * s.d * 2);
+    p.many.qexp = (int8_t*)part + p.bytes;
+    p.bytes = align_up(p.bytes + (size_t)s.n_tokens * s.Hq);
     p.many.min_rows = rows + 1;
     p.many.max_rows = INT32_MAX;
     p.few.max_rows = rows;

@@ -21,8 +21,13 @@
 // f16, and O is rescaled a few times in a row's life and not once per tile.
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of a half (a
-// thread per row), warps 8-11 queries (rotation, f16) and cache tiles (codes
-// to f16), warp 12 issues the MMAs, warp 13 copies pages to shared memory.
+// thread per row), warps 8-11 cache tiles (codes to f16), warp 12 issues the
+// MMAs, warp 13 copies queries and pages to shared memory.  Each role's loop is
+// kept short: unrolled over a whole tile they came to 40 KB, and waiting for
+// instructions was the largest stall.
+//
+// The queries are rotated by a kernel before (page_rotate_kernel): with a row
+// block's rotation inside the attention, every unit began with 25 us of it.
 #include "page.cuh"
 #include "tc.cuh"
 
@@ -38,7 +43,8 @@ constexpr float kSlack = 8.f;   // log2 units
 struct alignas(16) TileScales {  // read by float4
   float ks[8], ve[8], ive[8];  // key scale; value scale f * 2^e: e, 2^-e
   uint32_t vf[8];              // f, twice in f16
-  uint32_t loaded, pad[3];     // groups that were loaded (bits)
+  uint32_t loaded;             // groups that were loaded (bits)
+  bool neg, plain;             // a key scale is negative; all f are 1
 };
 
 // A segment: a piece of one unit, this CTA's tiles of it.  Warp 13 writes them.
@@ -56,7 +62,6 @@ struct alignas(16) Segment {
 constexpr int kSegments = 8;
 
 struct Shared {
-  int8_t qexp[2][256];  // by segment parity: exponent of the row's power of two
   Segment segments[kSegments];
   TileScales meta[kRing];
   uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
@@ -103,18 +108,112 @@ __device__ __forceinline__ bool has_nan(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
 }
 
+// Two fp32 at a time.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float m, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *(const uint32_t*)&h;
 }
 
+// Queries of the sequences that this file's attention takes, rotated, as f16
+// times a power of two for each row: qrot [n_tokens][Hq][d], exponents
+// qexp [n_tokens][Hq].  A warp per token: lanes hold two (d = 64: one) pairs,
+// whose cos and sin serve all heads.  Bound by memory: 2 bytes in, 2 out.
+constexpr int kRotateWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kRotateWarps * 32)
+page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
+                   const __nv_bfloat16* __restrict__ q, int64_t q_stride) {
+  constexpr int kP = D / 64;  // pairs of a lane
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kRotateWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (t >= s.n_tokens) return;
+  // the last sequence whose first row is at or before t, by 32 tries at a time
+  int b = 0, n = s.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, k = b + lane * step;
+    const bool at = k < b + n && (s.offs[k] <= t);
+    const int hit = max(__popc(__ballot_sync(0xffffffffu, at)) - 1, 0);
+    n = min(step, n - hit * step);
+    b += hit * step;
+  }
+  const PageSeq sq = page_seq(s, b);
+  const int64_t rows = (int64_t)sq.m * s.G;
+  if (rows < w.min_rows || rows > w.max_rows || t < sq.row0 || t >= sq.row0 + sq.m) return;
+  const int pos = sq.n - sq.m + (t - sq.row0);
+  float c[kP], sn[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    c[i] = 1.f, sn[i] = 0.f;
+    if (s.rotate && pos >= 0) page_cs(pos, s.turns[kP * lane + i], c[i], sn[i]);
+  }
+  const __nv_bfloat16* src = q + (int64_t)t * q_stride + kP * lane;
+  __half* dst = (__half*)w.qrot + (int64_t)t * s.Hq * D + kP * lane;
+  constexpr int kBatch = 4;  // rows in flight
+  for (int h0 = 0; h0 < s.Hq; h0 += kBatch) {
+    float x[kBatch][kP], y[kBatch][kP];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = min(h0 + j, s.Hq - 1);
+      if constexpr (kP == 2) {
+        const uint32_t a = *(const uint32_t*)(src + h * D), b2 = *(const uint32_t*)(src + h * D + D / 2);
+        x[j][0] = __uint_as_float(a << 16), x[j][1] = __uint_as_float(a & 0xFFFF0000u);
+        y[j][0] = __uint_as_float(b2 << 16), y[j][1] = __uint_as_float(b2 & 0xFFFF0000u);
+      } else {
+        x[j][0] = __bfloat162float(src[h * D]);
+        y[j][0] = __bfloat162float(src[h * D + D / 2]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j;
+      float am = 0.f;
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const float a = x[j][i] * c[i] - y[j][i] * sn[i], b2 = y[j][i] * c[i] + x[j][i] * sn[i];
+        x[j][i] = a, y[j][i] = b2;
+        am = fmaxf(am, fmaxf(fabsf(a), fabsf(b2)));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      // power of two that brings the row's largest element into [2^7, 2^8)
+      int ex = (int)(__float_as_uint(am) >> 23) - 127 - 7;
+      ex = min(max(ex, -119), 119);
+      const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
+      if (h < s.Hq) {
+        if constexpr (kP == 2) {
+          *(uint32_t*)(dst + h * D) = half2_bits(x[j][0] * mul, x[j][1] * mul);
+          *(uint32_t*)(dst + h * D + D / 2) = half2_bits(y[j][0] * mul, y[j][1] * mul);
+        } else {
+          dst[h * D] = __float2half_rn(x[j][0] * mul);
+          dst[h * D + D / 2] = __float2half_rn(y[j][0] * mul);
+        }
+        if (lane == 0) w.qexp[(int64_t)t * s.Hq + h] = (int8_t)ex;
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
-                 const __nv_bfloat16* __restrict__ q, int64_t q_stride,
-                 const uint8_t* __restrict__ k_pages, const uint8_t* __restrict__ v_pages,
-                 const float* __restrict__ k_scales, const float* __restrict__ v_scales,
-                 __nv_bfloat16* __restrict__ out) {
+                 const __grid_constant__ CUtensorMap qmap, const uint8_t* __restrict__ k_pages,
+                 const uint8_t* __restrict__ v_pages, const float* __restrict__ k_scales,
+                 const float* __restrict__ v_scales, __nv_bfloat16* __restrict__ out) {
   using C = Many<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared& sh = *(Shared*)(smem + C::kOffShared);
@@ -147,11 +246,12 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       tc::mbar_init(cfull(i), 1);
       tc::mbar_init(cfree(i), kConvert);
     }
-    tc::mbar_init(qfull, kConvert);
+    tc::mbar_init(qfull, 1);
     tc::mbar_init(qfree, 1);
     for (int i = 0; i < kSegments; ++i) tc::mbar_init(segfull(i), 1);
     tc::mbar_fence_init();
   }
+  if (warp == 13 && lane == 0) tc::tma_prefetch_desc(&qmap);
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), C::kTmem);
   if (tid < 2 * kRing * 4) sh.nan[tid / 4][tid % 4] = 0;
   grid_dependency_wait();
@@ -176,9 +276,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       wait(segfull(i), (i / kSegments) & 1);
       return sh.segments[i % kSegments];
     };
-    // 200 * 256 + 72 * 128 + 40 * 128 = 128 * 512 registers
     if (warp >= 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
       // ------------------------------------------------ MMA issuer
       if (warp == 12 && tc::elect_one()) {
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, kPageTile, false);
@@ -289,23 +387,42 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
             const size_t src = (((size_t)max(pg, 0) * s.U + cur.u) * s.T) * D;
             const uint32_t dst = sm0 + C::kOffCodes + lane * 16 * D;
+            const bool neg = __any_sync(0xffffffffu, ks < 0.f);
+            // zeros and what is not finite keep e = 0
+            int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
+            if (e < -100 || e > 100) e = 0;
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23), f = vs * down;
+            const bool plain = __all_sync(0xffffffffu, pg < 0 || f == 1.f);
             wait(cfree(0), (it & 1) ^ 1);
+            if (lane == 0) {
+              TileScales& mt = meta[it & (kRing - 1)];
+              mt.loaded = loaded;
+              mt.neg = neg;
+              mt.plain = plain;
+            }
             if (lane < 8) {
               TileScales& mt = meta[it & (kRing - 1)];
-              // zeros and what is not finite keep e = 0
-              int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
-              if (e < -100 || e > 100) e = 0;
-              const float down = __uint_as_float((uint32_t)(127 - e) << 23);
               mt.ks[lane] = ks;
               mt.ve[lane] = (float)e;
               mt.ive[lane] = down;
-              mt.vf[lane] = half2_bits(vs * down, vs * down);
-              if (lane == 0) mt.loaded = loaded;
+              mt.vf[lane] = half2_bits(f, f);
             }
             __syncwarp();
             if (lane == 0) tc::mbar_expect_tx(cfull(0), bytes);
             __syncwarp();
             if (first && !dead) tc::bulk_load(dst, k_pages + src, (uint32_t)(s.T * D), cfull(0));
+            if (i == 0) {
+              if (seg > 0) wait(qfree, (seg - 1) & 1);
+              if (lane == 0) {
+                // whole boxes count, what lies behind the last row included
+                tc::mbar_expect_tx(qfull, dead ? 0u : (uint32_t)(2 * tb2 * s.G * D * 2));
+                if (!dead)
+                  for (int j = 0; j < 2 * (D / 64); ++j)
+                    tc::tma_load_3d(sm0 + j * 16384, &qmap, j % (D / 64) * 64, cur.u * s.G,
+                                    cur.row0 + cur.k * w.tb + j / (D / 64) * tb2, qfull);
+              }
+              __syncwarp();
+            }
             wait(cfree(1), (it & 1) ^ 1);
             __syncwarp();
             const uint32_t vbytes = __any_sync(0xffffffffu, dead) ? 0u : bytes;
@@ -327,18 +444,13 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       }
       __syncwarp();
     } else if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      // ------------------------------------------------ queries and cache tiles
+      // ------------------------------------------------ cache tiles
       constexpr int kCols = D / 16;            // 16-code chunks of a row
       constexpr int kRows = kConvert / kCols;  // rows of a pass
       constexpr int kPass = kPageTile / kRows;
-      const int ct = tid - 256, cw = warp - 8;
+      constexpr int kBatch = 4;                // passes whose codes are read together
+      const int ct = tid - 256;
       const int col = ct % kCols, row = ct / kCols;
-      // queries: a row's pairs over kLanes lanes, two to a lane
-      constexpr int kLanes = D / 4;
-      const int ql = lane % kLanes;
-      const double turn0 = s.turns[2 * ql], turn1 = s.turns[2 * ql + 1];
-
       for (int seg = 0;; ++seg) {
         const Segment& sg = segment(seg);
         const int n = dead ? 0 : sg.n;
@@ -356,67 +468,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           *(uint4*)(smem + (flip ? o1 : o0)) = flip ? bq : a;
           *(uint4*)(smem + (flip ? o0 : o1)) = flip ? a : bq;
         };
-        // ---- queries
-        if (seg > 0) wait(qfree, (seg - 1) & 1);
-        {
-          const int live = (p1 - p0 + 1) * s.G;  // rows
-          const int groups = 4 * (32 / kLanes);
-          const int per = (2 * tb2 * s.G + groups - 1) / groups;
-          const int r0 = (cw * (32 / kLanes) + lane / kLanes) * per;
-          int i = r0 / s.G, g = r0 - i * s.G, had = -1;
-          float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
-          constexpr int kBatch = 8;
-          for (int a0 = 0; a0 < per; a0 += kBatch) {
-            uint32_t xa[kBatch], xb[kBatch];
-            int i2 = i, g2 = g;
-#pragma unroll
-            for (int a = 0; a < kBatch; ++a) {
-              xa[a] = xb[a] = 0;
-              if (a0 + a < per && r0 + a0 + a < live) {
-                const __nv_bfloat16* src = q + (int64_t)(sg.row + i2) * q_stride + (sg.u * s.G + g2) * D + 2 * ql;
-                xa[a] = *(const uint32_t*)src;
-                xb[a] = *(const uint32_t*)(src + D / 2);
-              }
-              if (++g2 == s.G) g2 = 0, ++i2;
-            }
-#pragma unroll
-            for (int a = 0; a < kBatch; ++a) {
-              const bool here = a0 + a < per && r0 + a0 + a < live;
-              if (s.rotate && here && i != had) {
-                page_cs(p0 + i, turn0, c0, s0);
-                page_cs(p0 + i, turn1, c1, s1);
-                had = i;
-              }
-              const float a0f = __uint_as_float(xa[a] << 16), a1f = __uint_as_float(xa[a] & 0xFFFF0000u);
-              const float b0f = __uint_as_float(xb[a] << 16), b1f = __uint_as_float(xb[a] & 0xFFFF0000u);
-              const float y0 = a0f * c0 - b0f * s0, y1 = a1f * c1 - b1f * s1;
-              const float z0 = b0f * c0 + a0f * s0, z1 = b1f * c1 + a1f * s1;
-              float am = fmaxf(fmaxf(fabsf(y0), fabsf(y1)), fmaxf(fabsf(z0), fabsf(z1)));
-#pragma unroll
-              for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-              // power of two that brings the row's largest element into [2^7, 2^8)
-              int ex = (int)(__float_as_uint(am) >> 23) - 127 - 7;
-              ex = min(max(ex, -119), 119);
-              const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
-              if (here) {
-                const int h = i >= tb2, r = (i - (h ? tb2 : 0)) * s.G + g;  // row in the half
-                if (ql == 0) sh.qexp[seg & 1][h * 128 + r] = (int8_t)ex;
-                unsigned char* dst = smem + h * C::kQHalf + r * 128;
-                const int sw = (r & 7) << 4;
-                *(uint32_t*)(dst + ((4 * ql) ^ sw)) = half2_bits(y0 * mul, y1 * mul);
-                if constexpr (D == 128)
-                  *(uint32_t*)(dst + 16384 + ((4 * ql) ^ sw)) = half2_bits(z0 * mul, z1 * mul);
-                else
-                  *(uint32_t*)(dst + ((4 * ql + 64) ^ sw)) = half2_bits(z0 * mul, z1 * mul);
-              }
-              if (++g == s.G) g = 0, ++i;
-            }
-          }
-        }
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(qfull);
-
-        // ---- tiles
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it & 1;
           const int64_t tile0 = first + (int64_t)i * kPageTile;
@@ -436,45 +487,58 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           wait(kfree(st), ((it >> 1) & 1) ^ 1);
           // a later tile's; all have left the slot's last one, and none is there yet
           if (ct < 4) sh.nan[(it + 2) & (2 * kRing - 1)][ct] = 0;
+#pragma unroll 1
+          for (int j = 0; j < kPass; j += kBatch) {
+            uint4 c[kBatch];
 #pragma unroll
-          for (int j = 0; j < kPass; ++j) {
-            const int rr = j * kRows + row;
-            const uint32_t f = (__float_as_uint(mt.ks[rr >> 4]) >> 31) * 0x80008000u;  // its sign
-            uint32_t x[8];
-            widen16(codes(0, j), x);
+            for (int k = 0; k < kBatch; ++k) c[k] = codes(0, j + k);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] ^= f;
-            store(C::kOffK + st * C::kTileBytes, rr, x);
+            for (int k = 0; k < kBatch; ++k) {
+              uint32_t x[8];
+              widen16(c[k], x);
+              store(C::kOffK + st * C::kTileBytes, (j + k) * kRows + row, x);
+            }
           }
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(cfree(0));
           tc::mbar_arrive(kfull(st));
           wait(cfull(1), it & 1);
           wait(vfree(st), ((it >> 1) & 1) ^ 1);
+#pragma unroll 1
+          for (int j = 0; j < kPass; j += kBatch) {
+            uint4 c[kBatch];
 #pragma unroll
-          for (int j = 0; j < kPass; ++j) {
-            const int rr = j * kRows + row;
-            uint4 c = codes(1, j);
+            for (int k = 0; k < kBatch; ++k) c[k] = codes(1, j + k);
             if (!full) {
               // Rows differ in what they see.  A NaN would not be hidden by a
               // weight of zero: such a token's values become zeros, and the NaN is
               // handed to the rows that see it by their weights.
-              const bool bad = has_nan(c.x) || has_nan(c.y) || has_nan(c.z) || has_nan(c.w);
-              const uint32_t any = __ballot_sync(0xffffffffu, bad);
-              if ((any >> (lane / kCols * kCols)) & ((1u << kCols) - 1u)) {
-                c = make_uint4(0, 0, 0, 0);
-                if (col == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const int rr = (j + k) * kRows + row;
+                const bool bad = has_nan(c[k].x) || has_nan(c[k].y) || has_nan(c[k].z) || has_nan(c[k].w);
+                const uint32_t any = __ballot_sync(0xffffffffu, bad);
+                if ((any >> (lane / kCols * kCols)) & ((1u << kCols) - 1u)) {
+                  c[k] = make_uint4(0, 0, 0, 0);
+                  if (col == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
+                }
               }
             }
-            const uint32_t f = mt.vf[rr >> 4];
-            uint32_t x[8];
-            widen16(c, x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const __half2 y = __hmul2(*(const __half2*)&x[k], *(const __half2*)&f);
-              x[k] = *(const uint32_t*)&y;
+            for (int k = 0; k < kBatch; ++k) {
+              const int rr = (j + k) * kRows + row;
+              uint32_t x[8];
+              widen16(c[k], x);
+              if (!mt.plain) {
+                const uint32_t f = mt.vf[rr >> 4];
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2) {
+                  const __half2 y = __hmul2(*(const __half2*)&x[i2], *(const __half2*)&f);
+                  x[i2] = *(const uint32_t*)&y;
+                }
+              }
+              store(C::kOffV + st * C::kTileBytes, rr, x);
             }
-            store(C::kOffV + st * C::kTileBytes, rr, x);
           }
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(cfree(1));
@@ -482,7 +546,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         }
       }
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
       // ------------------------------------------------ softmax
       const int h = warp >> 2, r = tid & 127;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -499,46 +562,61 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         const int pos = live ? p0 + ti : -1;
         const int see_lo = s.window && live ? max(pos - s.window + 1, 0) : 0;
         if (h == 0 || p1 - p0 >= tb2) {
-          float m = -INFINITY, l = 0.f, fac = 0.f;
+          float m = -INFINITY, l = 0.f;
+          // softmax scale * log2(e) * the row's power of two
+          float fac = s.scale * 1.4426950408889634f;
+          if (live)
+            fac *= __uint_as_float((uint32_t)(127 + w.qexp[(int64_t)(sg.row + ti) * s.Hq + sg.u * s.G + rg]) << 23);
           for (int i = 0; i < n; ++i, ++cnt) {
             const TileScales& mt = meta[(it + i) & (kRing - 1)];
             const int64_t tile0 = (int64_t)(sg.t0 + i) * kPageTile;
             wait(sready(h), cnt & 1);
             tc::fence_after_sync();
-            if (i == 0)
-              fac = s.scale * 1.4426950408889634f *
-                    __uint_as_float((uint32_t)(127 + sh.qexp[seg & 1][h * 128 + r]) << 23);
-            float t[kPageTile];
-#pragma unroll
-            for (int c = 0; c < kPageTile; c += 32) tc::tmem_ld32(cs + c, t + c);
+            // t = S * c + e by group of 16 tokens; where tokens are masked (or a key scale
+            // is negative) t itself takes S's place
             const uint32_t loaded = mt.loaded;
-            tc::tmem_ld_wait();
-            // t = S * c + e by group of 16 tokens, but where tokens are masked: t itself
-            const bool masked = !(tile0 >= sg.all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu);
-            if (masked) {
-              const int hi = (int)max(min((int64_t)pos - tile0, (int64_t)kPageTile), (int64_t)-1);
-              const int lo = (int)max(min((int64_t)see_lo - tile0, (int64_t)kPageTile), (int64_t)0);
-              wait(vfull((it + i) & 1), ((it + i) >> 1) & 1);  // the NaN bits
+            const bool masked =
+                !(tile0 >= sg.all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu) || mt.neg;
+            if (masked) wait(vfull((it + i) & 1), ((it + i) >> 1) & 1);  // the NaN bits
+            constexpr int kW = 64;  // columns at a time
+            float mt_ = -INFINITY;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kPageTile; c0 += kW) {
+              float t[kW];
+              tc::tmem_ld32(cs + c0, t);
+              tc::tmem_ld32(cs + c0 + 32, t + 32);
+              tc::tmem_ld_wait();
+              if (masked) {
+                const int hi = (int)max(min((int64_t)pos - tile0 - c0, (int64_t)kW), (int64_t)-1);
+                const int lo = (int)max(min((int64_t)see_lo - tile0 - c0, (int64_t)kW), (int64_t)0);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float c = fabsf(mt.ks[k]) * fac, e = mt.ve[k];
-                const int top = (loaded >> k) & 1u ? hi : -1;
-                const uint32_t nan = sh.nan[(it + i) & (2 * kRing - 1)][k >> 1] >> (16 * (k & 1));
+                for (int k = 0; k < kW / 16; ++k) {
+                  const int g = c0 / 16 + k;
+                  const float c = mt.ks[g] * fac, e = mt.ve[g];
+                  const int top = (loaded >> g) & 1u ? hi : -1;
+                  const uint32_t nan = sh.nan[(it + i) & (2 * kRing - 1)][g >> 1] >> (16 * (g & 1));
+                  uint32_t y[16];
 #pragma unroll
-                for (int j = 16 * k; j < 16 * k + 16; ++j) {
-                  float y = fmaf(t[j], c, e);
-                  if ((nan >> (j & 15)) & 1u) y = __uint_as_float(0x7FC00000u);
-                  t[j] = j <= top && j >= lo ? y : -INFINITY;
+                  for (int j = 0; j < 16; ++j) {
+                    float a = fmaf(t[16 * k + j], c, e);
+                    if ((nan >> j) & 1u) a = __uint_as_float(0x7FC00000u);
+                    a = 16 * k + j <= top && 16 * k + j >= lo ? a : -INFINITY;
+                    mt_ = fmaxf(mt_, a);
+                    y[j] = __float_as_uint(a);
+                  }
+                  tc::tmem_st16(cs + c0 + 16 * k, y);
+                }
+                tc::tmem_st_wait();
+              } else {
+#pragma unroll
+                for (int k = 0; k < kW / 16; ++k) {
+                  float a = t[16 * k];
+#pragma unroll
+                  for (int j = 1; j < 15; j += 2) a = fmaxf(fmaxf(a, t[16 * k + j]), t[16 * k + j + 1]);
+                  a = fmaxf(a, t[16 * k + 15]);
+                  mt_ = fmaxf(mt_, fmaf(a, mt.ks[c0 / 16 + k] * fac, mt.ve[c0 / 16 + k]));
                 }
               }
-            }
-            float mt_ = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float a = t[16 * k];
-#pragma unroll
-              for (int j = 1; j < 16; ++j) a = fmaxf(a, t[16 * k + j]);
-              mt_ = fmaxf(mt_, masked ? a : fmaf(a, fabsf(mt.ks[k]) * fac, mt.ve[k]));
             }
             const bool grow = mt_ > m + kSlack || (m == -INFINITY && mt_ > m);
             if (__any_sync(0xffffffffu, grow)) {
@@ -560,23 +638,31 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               }
             }
             const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kPageTile; c0 += kW) {
+              float t[kW];
+              tc::tmem_ld32(cs + c0, t);
+              tc::tmem_ld32(cs + c0 + 32, t + 32);
+              tc::tmem_ld_wait();
+              uint32_t pk[kW / 2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float c = masked ? 1.f : fabsf(mt.ks[k]) * fac, d = (masked ? 0.f : mt.ve[k]) - ref;
-              float sum = 0.f;
+              for (int k = 0; k < kW / 16; ++k) {
+                const int g = c0 / 16 + k;
+                const float c = masked ? 1.f : mt.ks[g] * fac, d = (masked ? 0.f : mt.ve[g]) - ref;
+                float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-              for (int j = 16 * k; j < 16 * k + 16; ++j) {
-                t[j] = ex2(fmaf(t[j], c, d));
-                sum += t[j];
+                for (int j = 16 * k; j < 16 * k + 16; j += 2) {
+                  fma2(t[j], t[j + 1], c, d);
+                  t[j] = ex2(t[j]);
+                  t[j + 1] = ex2(t[j + 1]);
+                  add2(sum0, sum1, t[j], t[j + 1]);
+                  pk[j / 2] = half2_bits(t[j], t[j + 1]);
+                }
+                l = fmaf(sum0 + sum1, mt.ive[g], l);
               }
-              l = fmaf(sum, mt.ive[k], l);
-              if (k & 1) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  pk[j] = half2_bits(t[16 * (k - 1) + 2 * j], t[16 * (k - 1) + 2 * j + 1]);
-                tc::tmem_st16(cs + 8 * (k - 1), pk);
-              }
+              // the weights take the place of scores that have been read
+              tc::tmem_st16(cs + c0 / 2, *(const uint32_t(*)[16])pk);
+              tc::tmem_st16(cs + c0 / 2 + 16, *(const uint32_t(*)[16])(pk + 16));
             }
             tc::tmem_st_wait();
             tc::fence_before_sync();
@@ -636,11 +722,15 @@ cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t 
                    cudaStream_t stream) {
   static int done[kMaxDevices];
   auto kern = page_many_kernel<D>;
-  const cudaError_t e = ensure_smem(kern, Many<D>::kSmem, done);
+  cudaError_t e = ensure_smem(kern, Many<D>::kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(kPageGrid), dim3(kThreads), Many<D>::kSmem, stream, true, s, w,
-                  (const __nv_bfloat16*)q, q_stride, (const uint8_t*)kp, (const uint8_t*)vp, ks, vs,
-                  (__nv_bfloat16*)out);
+  CUtensorMap qm;
+  if (!make_tmap_f16_heads(&qm, w.qrot, s.n_tokens, s.Hq, D, w.tb / 2, s.G)) return cudaErrorInvalidValue;
+  e = launch_k(page_rotate_kernel<D>, dim3((unsigned)((s.n_tokens + kRotateWarps - 1) / kRotateWarps)),
+               dim3(kRotateWarps * 32), 0, stream, true, s, w, (const __nv_bfloat16*)q, q_stride);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(kPageGrid), dim3(kThreads), Many<D>::kSmem, stream, true, s, w, qm,
+                  (const uint8_t*)kp, (const uint8_t*)vp, ks, vs, (__nv_bfloat16*)out);
 }
 
 }  // namespace

@@ -101,6 +101,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// The same of a 3-D tensor: z the outermost coordinate.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
 // Gather 4 rows (row0..row3, any order) of a 2-D tensor whose box is
 // {64 elements x 1 row}: 4 x 128 bytes land at dst, dst+128, dst+256, dst+384.
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int32_t x,
@@ -462,5 +472,10 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64
 // a box, swizzled over 64 or 128 bytes.
 bool make_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t cols,
                        uint32_t box_rows);
+
+// f16 [tokens][heads][d], d = 64 or 128: boxes of 64 elements x box_heads x
+// box_tokens, 128-byte swizzle.
+bool make_tmap_f16_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,
+                         uint32_t d, uint32_t box_tokens, uint32_t box_heads);
 
 }  // namespace salsc

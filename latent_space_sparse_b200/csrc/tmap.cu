@@ -61,4 +61,23 @@ bool make_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32
   return true;
 }
 
+bool make_tmap_f16_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,
+                         uint32_t d, uint32_t box_tokens, uint32_t box_heads) {
+  std::call_once(g_once, load_encode);
+  if (!g_encode) return false;
+  if (((uintptr_t)base & 15u) || (d != 64 && d != 128)) return false;
+  cuuint64_t dims[3] = {d, heads, tokens};
+  cuuint64_t strides[2] = {d * sizeof(uint16_t), heads * d * sizeof(uint16_t)};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUtensorMap m;
+  CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return false;
+  *map = m;
+  return true;
+}
+
 }  // namespace salsc
