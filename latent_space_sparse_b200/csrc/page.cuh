@@ -127,6 +127,7 @@ __device__ __forceinline__ void page_cs(int pos, double turns, float& c, float& 
 struct PageWork {
   int min_rows, max_rows;  // sequences with min_rows <= new tokens * G <= max_rows
   int tb;                  // new tokens of a row block
+  int over;                // tiles' worth of time that a unit takes besides its tiles
   int rows;                // rows of a partial slot (>= tb * G)
   // Partial results of units that several CTAs share: CTA c's slots 2c (a
   // piece that starts inside a unit) and 2c + 1 (one that starts a unit and
@@ -148,20 +149,29 @@ struct PageCursor {
   int row0;         // row of the sequence's first new token
   int tiles;        // tiles of the unit
   int tile;         // tile inside the unit (0-based from the block's first tile)
+  int64_t base;     // the unit's first place in the list
 
   __device__ __forceinline__ PageCursor(const PageStep& s_, const PageWork& w_) : s(s_), w(w_) {}
   __device__ __forceinline__ void load() {
     const PageSeq q = page_seq(s, b);
-    blk = PageBlocks{q.n, q.m, w.tb, s.window};
+    blk = PageBlocks{q.n, q.m, w.tb, s.window, w.over};
     row0 = q.row0;
   }
   __device__ __forceinline__ bool mine() const {
     const int64_t r = (int64_t)blk.m * s.G;
     return r >= w.min_rows && r <= w.max_rows;
   }
+  // tiles from `tile` on of a range that ends at place x1 (0 or less: none)
+  __device__ __forceinline__ int upto(int64_t x1) const {
+    return (int)(min((int64_t)tiles, x1 - base - w.over) - tile);
+  }
+  __device__ __forceinline__ bool whole(int n) const { return tile == 0 && n == tiles; }
+  // the unit's last tile's place
+  __device__ __forceinline__ int64_t last() const { return base + w.over + tiles - 1; }
   // to the next unit; false past the last one
   __device__ __forceinline__ bool next_unit() {
     tile = 0;
+    base += w.over + tiles;
     if (++u < s.U) return true;
     u = 0;
     if (++k < blk.count()) {
@@ -184,12 +194,12 @@ __device__ __forceinline__ int64_t page_seq_tiles(const PageStep& s, const PageW
   const PageSeq q = page_seq(s, b);
   const int64_t r = (int64_t)q.m * s.G;
   if (r < w.min_rows || r > w.max_rows) return 0;
-  const PageBlocks p{q.n, q.m, w.tb, s.window};
+  const PageBlocks p{q.n, q.m, w.tb, s.window, w.over};
   return (int64_t)s.U * p.before(p.count());
 }
 
-// Block-wide: the total number of tiles of the kernel's sequences, this CTA's
-// range of them [x0, x1), and where x0 lies (b, and the tile's index within
+// Block-wide: the length of the list of the kernel's sequences, this CTA's
+// range of it [x0, x1), and where x0 lies (b, and the place's index within
 // sequence b); b = -1 for an empty range.  sm: (blockDim / 32 + 2) int64.
 __device__ __forceinline__ void page_share(const PageStep& s, const PageWork& w, int64_t* sm,
                                            int64_t& total, int64_t& x0, int64_t& x1, int& b,
@@ -242,9 +252,10 @@ __device__ __forceinline__ void page_share(const PageStep& s, const PageWork& w,
   rem = sm[warps + 1];
 }
 
-// Place a cursor on tile `rem` of sequence b.  Every lane of the warp calls it,
-// with the same arguments: the row block is found by 32 tries at a time.
-__device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem) {
+// Place a cursor on place `rem` of sequence b, which is place x0 of the list.
+// Every lane of the warp calls it, with the same arguments: the row block is
+// found by 32 tries at a time.
+__device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem, int64_t x0) {
   c.b = b;
   c.load();
   // the row block: its U KV heads have U * tiles(k) tiles behind U * before(k)
@@ -260,8 +271,11 @@ __device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem) {
   c.k = lo;
   c.tiles = c.blk.tiles(c.k);
   rem -= (int64_t)c.s.U * c.blk.before(c.k);
-  c.u = (int)div_small(rem, c.tiles);
-  c.tile = (int)(rem - (int64_t)c.u * c.tiles);
+  const int cost = c.w.over + c.tiles;
+  c.u = (int)div_small(rem, cost);
+  rem -= (int64_t)c.u * cost;
+  c.base = x0 - rem;
+  c.tile = rem > c.w.over ? (int)(rem - c.w.over) : 0;
 }
 
 // Host side: launchers.

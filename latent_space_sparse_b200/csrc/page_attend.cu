@@ -6,6 +6,8 @@ namespace salsc {
 namespace {
 
 constexpr int kMergeWarps = 4;  // rows of a merge CTA
+// What a unit takes besides its tiles, in tiles.
+constexpr int kOverFew = 2, kOverMany = 3;
 
 // out[row] = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i over the pieces i
 // of a unit.  CTA c's second slot holds a unit's first piece, the following
@@ -95,6 +97,7 @@ Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
   const int rows = page_few_rows(s, dt);
   p.few = layout(s, rows, part, p.bytes);
   p.few.tb = rows / s.G;
+  p.few.over = kOverFew;
   p.few.min_rows = 1;
   p.few.max_rows = INT32_MAX;
   p.has_many = dt == SALSC_BF16 && (int64_t)s.max_q * s.G > rows;
@@ -105,6 +108,7 @@ Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
     p.bytes = align_up(p.bytes + (size_t)s.n_tokens * s.Hq * s.d * 2);
     p.many.qexp = (int8_t*)part + p.bytes;
     p.bytes = align_up(p.bytes + (size_t)s.n_tokens * s.Hq);
+    p.many.over = kOverMany;
     p.many.min_rows = rows + 1;
     p.many.max_rows = INT32_MAX;
     p.few.max_rows = rows;

@@ -138,15 +138,15 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
 
   if (x0 < x1) {
     PageCursor cur(s, w);
-    page_seek(cur, b, rem);
-    int64_t left = x1 - x0;
+    page_seek(cur, b, rem, x0);
     int it = 0;  // tiles so far
     const int npg = kPageTile / s.T;
 
     if (warp == 4) {
       // ------------------------------------------------ TMA producer
       while (true) {
-        const int n = (int)min((int64_t)(cur.tiles - cur.tile), left);
+        const int n = cur.upto(x1);
+        if (n <= 0) break;
         const int t0 = cur.blk.tile0(cur.k) + cur.tile;
         const int lo = cur.blk.lo(cur.k), hi = cur.blk.pos1(cur.k);
         // a batch of 32 pages: lane i holds page i; its loads fly one batch ahead
@@ -204,8 +204,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           ks = ks_n;
           vs = vs_n;
         }
-        left -= n;
-        if (left <= 0 || !cur.next_unit()) break;
+        if (!cur.next_unit()) break;
       }
     } else if (warp == 5) {
       // ------------------------------------------------ MMA issuer
@@ -244,15 +243,15 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           tc::mma_commit(free_(st));
         };
         for (int seg = 0;; ++seg) {
-          const int n = (int)min((int64_t)(cur.tiles - cur.tile), left);
+          const int n = cur.upto(x1);
+        if (n <= 0) break;
           wait(qready, seg & 1);
           scores(it);
           for (int i = 0; i < n; ++i, ++it) {
             if (i + 1 < n) scores(it + 1);
             values(it, i == 0);
           }
-          left -= n;
-          if (left <= 0 || !cur.next_unit()) break;
+          if (!cur.next_unit()) break;
         }
       }
       __syncwarp();
@@ -260,9 +259,9 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
       // ------------------------------------------------ softmax
       const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
       const int weff = s.window ? s.window : INT32_MAX;
-      int64_t x = x0;
       while (true) {
-        const int n = (int)min((int64_t)(cur.tiles - cur.tile), left);
+        const int n = cur.upto(x1);
+        if (n <= 0) break;
         const int t0 = cur.blk.tile0(cur.k) + cur.tile;
         const int p0 = cur.blk.pos0(cur.k), p1 = cur.blk.pos1(cur.k);
         const int rows = (p1 - p0 + 1) * s.G;
@@ -508,7 +507,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         wait(pvdone((it - 1) & 1), ((it - 1) >> 1) & 1);
         tc::fence_after_sync();
         tc::named_sync(1, kSoftmax);
-        const bool whole = cur.tile == 0 && n == cur.tiles;
+        const bool whole = cur.whole(n);
         const int slot = 2 * blockIdx.x + (cur.tile == 0 ? 1 : 0);
         if (!whole && tid < rows) {
           float mm = 0.f;
@@ -520,7 +519,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         }
         if (tid == 0 && !whole && cur.tile == 0)
           w.info[blockIdx.x] = make_int4(row0, cur.u, rows,
-                                         (int)share_of_tile(x + cur.tiles - 1, total, gridDim.x));
+                                         (int)share_of_tile(cur.last(), total, gridDim.x));
         if (warp * 32 < D) {
 #pragma unroll
           for (int r0 = 0; r0 < RC; r0 += 4) {
@@ -553,9 +552,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         }
         tc::fence_before_sync();
         tc::named_sync(1, kSoftmax);  // wsum, qfac, rpos, rout are free
-        left -= n;
-        x += n;
-        if (left <= 0 || !cur.next_unit()) break;
+        if (!cur.next_unit()) break;
       }
     }
   }

@@ -108,6 +108,13 @@ __device__ __forceinline__ bool has_nan(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
 }
 
+// 32 bytes, the size of a sector: rows are apart, a thread has one to itself.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Two fp32 at a time.
 __device__ __forceinline__ void fma2(float& a0, float& a1, float m, float c) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
@@ -211,8 +218,8 @@ page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ P
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
-                 const __grid_constant__ CUtensorMap qmap, const uint8_t* __restrict__ k_pages,
-                 const uint8_t* __restrict__ v_pages, const float* __restrict__ k_scales,
+                 const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, const float* __restrict__ k_scales,
                  const float* __restrict__ v_scales, __nv_bfloat16* __restrict__ out) {
   using C = Many<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -251,7 +258,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
     for (int i = 0; i < kSegments; ++i) tc::mbar_init(segfull(i), 1);
     tc::mbar_fence_init();
   }
-  if (warp == 13 && lane == 0) tc::tma_prefetch_desc(&qmap);
+  if (warp == 13 && lane < 3) tc::tma_prefetch_desc(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), C::kTmem);
   if (tid < 2 * kRing * 4) sh.nan[tid / 4][tid % 4] = 0;
   grid_dependency_wait();
@@ -276,7 +283,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       wait(segfull(i), (i / kSegments) & 1);
       return sh.segments[i % kSegments];
     };
+    // 192 * 256 + 72 * 128 + 56 * 128 = 128 * 512 registers
     if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       // ------------------------------------------------ MMA issuer
       if (warp == 12 && tc::elect_one()) {
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, kPageTile, false);
@@ -343,10 +352,16 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       // ------------------------------------------------ pages to shared memory
       if (warp == 13) {
         PageCursor cur(s, w);
-        page_seek(cur, b, rem);
-        int64_t x = x0;
+        page_seek(cur, b, rem, x0);
         for (int seg = 0;; ++seg) {
-          const int n = (int)min((int64_t)(cur.tiles - cur.tile), x1 - x);
+          const int n = cur.upto(x1);
+          if (n <= 0) {
+            if (lane == 0) {
+              sh.segments[seg % kSegments].n = 0;
+              tc::mbar_arrive(segfull(seg));
+            }
+            break;
+          }
           const int t0 = cur.blk.tile0(cur.k) + cur.tile;
           const int p0 = cur.blk.pos0(cur.k), hi = cur.blk.pos1(cur.k), lo = cur.blk.lo(cur.k);
           if (lane == 0) {
@@ -356,13 +371,12 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             sg.row = cur.row0 + cur.k * w.tb;
             sg.u = (short)cur.u;
             sg.starts = cur.tile == 0;
-            sg.whole = cur.tile == 0 && n == cur.tiles;
+            sg.whole = cur.whole(n);
             tc::mbar_arrive(segfull(seg));
             if (cur.tile == 0 && n < cur.tiles)  // others go on with the unit
               w.info[blockIdx.x] = make_int4(cur.row0 + cur.k * w.tb, cur.u, (hi - p0 + 1) * s.G,
-                                             (int)share_of_tile(x + cur.tiles - 1, total, gridDim.x));
+                                             (int)share_of_tile(cur.last(), total, gridDim.x));
           }
-          x += n;
           // lane i: the page that holds group i % 8 of a tile, or -1; a page is copied
           // whole if a row sees any of it
           auto look = [&](int i) {
@@ -385,7 +399,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const uint32_t bytes = dead ? 0u : (uint32_t)__popc(loaded) * 16 * D;
             // a page's first group copies it (a tile holds whole pages)
             const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
-            const size_t src = (((size_t)max(pg, 0) * s.U + cur.u) * s.T) * D;
+            const int src = (pg * s.U + cur.u) * s.T;
             const uint32_t dst = sm0 + C::kOffCodes + lane * 16 * D;
             const bool neg = __any_sync(0xffffffffu, ks < 0.f);
             // zeros and what is not finite keep e = 0
@@ -410,7 +424,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             __syncwarp();
             if (lane == 0) tc::mbar_expect_tx(cfull(0), bytes);
             __syncwarp();
-            if (first && !dead) tc::bulk_load(dst, k_pages + src, (uint32_t)(s.T * D), cfull(0));
+            if (first && !dead) tc::tma_load_2d(dst, &kmap, 0, src, cfull(0));
             if (i == 0) {
               if (seg > 0) wait(qfree, (seg - 1) & 1);
               if (lane == 0) {
@@ -428,12 +442,11 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const uint32_t vbytes = __any_sync(0xffffffffu, dead) ? 0u : bytes;
             if (lane == 0) tc::mbar_expect_tx(cfull(1), vbytes);
             __syncwarp();
-            if (first && vbytes)
-              tc::bulk_load(dst + C::kCodeBytes, v_pages + src, (uint32_t)(s.T * D), cfull(1));
+            if (first && vbytes) tc::tma_load_2d(dst + C::kCodeBytes, &vmap, 0, src, cfull(1));
             pg = pg_next;
             scales();
           }
-          if (x >= x1 || !cur.next_unit()) {
+          if (!cur.next_unit()) {
             if (lane == 0) {
               sh.segments[(seg + 1) % kSegments].n = 0;
               tc::mbar_arrive(segfull(seg + 1));
@@ -444,13 +457,19 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       }
       __syncwarp();
     } else if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       // ------------------------------------------------ cache tiles
-      constexpr int kCols = D / 16;            // 16-code chunks of a row
-      constexpr int kRows = kConvert / kCols;  // rows of a pass
-      constexpr int kPass = kPageTile / kRows;
-      constexpr int kBatch = 4;                // passes whose codes are read together
+      // A pass is 32 rows by 64 codes: a warp's lanes hold 16 codes each of 8
+      // rows, and eight lanes that access shared memory together those of rows
+      // p and p ^ 5: the swizzles then send them to all banks, both for reading
+      // (rows that differ in bit 2) and for writing (in bit 0).
+      constexpr int kHalves = D / 64;
+      constexpr int kPass = 4 * kHalves;
+      constexpr int kBatch = 4;  // passes whose codes are read together
       const int ct = tid - 256;
-      const int col = ct % kCols, row = ct / kCols;
+      const int row = (warp - 8) * 8 + ((lane >> 3) ^ ((lane >> 2 & 1) * 5));
+      auto row_of = [&](int j) { return j / kHalves * 32 + row; };
+      auto col_of = [&](int j) { return j % kHalves * 4 + (lane & 3); };
       for (int seg = 0;; ++seg) {
         const Segment& sg = segment(seg);
         const int n = dead ? 0 : sg.n;
@@ -458,15 +477,11 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         const int p0 = sg.p0, p1 = sg.p1, lo = sg.lo, all_lo = sg.all_lo;
         const int64_t first = (int64_t)sg.t0 * kPageTile;
         // f16 rows into a swizzled tile: blocks of 64 elements (128 bytes) by row
-        auto store = [&](uint32_t tile, int rr, const uint32_t (&x)[8]) {
-          const int c = 2 * col;
-          const uint32_t base = tile + (uint32_t)(c >> 3) * 16384 + rr * 128;
-          const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), bq = make_uint4(x[4], x[5], x[6], x[7]);
-          // the upper columns store their second chunk first: eight lanes then hit all banks
-          const bool flip = col >= 4;
-          const uint32_t o0 = base + (((c & 7) ^ (rr & 7)) << 4), o1 = base + ((((c & 7) + 1) ^ (rr & 7)) << 4);
-          *(uint4*)(smem + (flip ? o1 : o0)) = flip ? bq : a;
-          *(uint4*)(smem + (flip ? o0 : o1)) = flip ? a : bq;
+        auto store = [&](uint32_t tile, int rr, int c, const uint32_t (&x)[8]) {
+          unsigned char* base = smem + tile + (c >> 2) * 16384 + rr * 128;
+          const int k = c * 2 & 7;
+          *(uint4*)(base + ((k ^ (rr & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *(uint4*)(base + (((k + 1) ^ (rr & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
         };
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it & 1;
@@ -478,9 +493,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           const bool full = tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu;
           // codes of pass j; zeros for tokens that no row sees
           auto codes = [&](int v, int j) {
-            const int rr = j * kRows + row;
+            const int rr = row_of(j), cc = col_of(j);
             const int64_t tok = tile0 + rr;
-            uint4 c = *(const uint4*)(smem + C::kOffCodes + v * C::kCodeBytes + rr * D + col * 16);
+            uint4 c = *(const uint4*)(smem + C::kOffCodes + v * C::kCodeBytes + rr * D +
+                                      ((cc ^ (D == 128 ? rr & 7 : rr >> 1 & 3)) << 4));
             if (!full && (tok < lo || tok > p1 || !((loaded >> (rr >> 4)) & 1u))) c = make_uint4(0, 0, 0, 0);
             return c;
           };
@@ -496,7 +512,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             for (int k = 0; k < kBatch; ++k) {
               uint32_t x[8];
               widen16(c[k], x);
-              store(C::kOffK + st * C::kTileBytes, (j + k) * kRows + row, x);
+              store(C::kOffK + st * C::kTileBytes, row_of(j + k), col_of(j + k), x);
             }
           }
           tc::fence_proxy_async_smem();
@@ -514,19 +530,22 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               // weight of zero: such a token's values become zeros, and the NaN is
               // handed to the rows that see it by their weights.
 #pragma unroll
-              for (int k = 0; k < kBatch; ++k) {
-                const int rr = (j + k) * kRows + row;
-                const bool bad = has_nan(c[k].x) || has_nan(c[k].y) || has_nan(c[k].z) || has_nan(c[k].w);
-                const uint32_t any = __ballot_sync(0xffffffffu, bad);
-                if ((any >> (lane / kCols * kCols)) & ((1u << kCols) - 1u)) {
-                  c[k] = make_uint4(0, 0, 0, 0);
-                  if (col == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
+              for (int k = 0; k < kBatch; k += kHalves) {
+                bool bad = false;
+#pragma unroll
+                for (int a = k; a < k + kHalves; ++a)
+                  bad |= has_nan(c[a].x) || has_nan(c[a].y) || has_nan(c[a].z) || has_nan(c[a].w);
+                if (__ballot_sync(0xffffffffu, bad) >> (lane & 28) & 15u) {  // the row's lanes
+#pragma unroll
+                  for (int a = k; a < k + kHalves; ++a) c[a] = make_uint4(0, 0, 0, 0);
+                  const int rr = row_of(j + k);
+                  if ((lane & 3) == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
                 }
               }
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-              const int rr = (j + k) * kRows + row;
+              const int rr = row_of(j + k);
               uint32_t x[8];
               widen16(c[k], x);
               if (!mt.plain) {
@@ -537,7 +556,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
                   x[i2] = *(const uint32_t*)&y;
                 }
               }
-              store(C::kOffV + st * C::kTileBytes, rr, x);
+              store(C::kOffV + st * C::kTileBytes, rr, col_of(j + k), x);
             }
           }
           tc::fence_proxy_async_smem();
@@ -546,6 +565,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         }
       }
     } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
       // ------------------------------------------------ softmax
       const int h = warp >> 2, r = tid & 127;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -578,45 +598,49 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const bool masked =
                 !(tile0 >= sg.all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu) || mt.neg;
             if (masked) wait(vfull((it + i) & 1), ((it + i) >> 1) & 1);  // the NaN bits
-            constexpr int kW = 64;  // columns at a time
-            float mt_ = -INFINITY;
+            if (masked) {
+              const int64_t top = min((int64_t)pos - tile0, (int64_t)kPageTile - 1);  // last token seen
+              const int bot = (int)max(min((int64_t)see_lo - tile0, (int64_t)kPageTile), (int64_t)0);
 #pragma unroll 1
-            for (int c0 = 0; c0 < kPageTile; c0 += kW) {
-              float t[kW];
-              tc::tmem_ld32(cs + c0, t);
-              tc::tmem_ld32(cs + c0 + 32, t + 32);
-              tc::tmem_ld_wait();
-              if (masked) {
-                const int hi = (int)max(min((int64_t)pos - tile0 - c0, (int64_t)kW), (int64_t)-1);
-                const int lo = (int)max(min((int64_t)see_lo - tile0 - c0, (int64_t)kW), (int64_t)0);
+              for (int c0 = 0; c0 < kPageTile; c0 += 32) {
+                float y[32];
+                tc::tmem_ld32(cs + c0, y);
+                const int hi = (int)max(top - c0, (int64_t)-1), lo = bot - c0;
+                uint32_t sees = hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(hi, 31));
+                if (lo > 0) sees &= lo > 31 ? 0u : 0xFFFFFFFFu << lo;
+                const int g = c0 / 16;
+                if (!((loaded >> g) & 1u)) sees &= 0xFFFF0000u;
+                if (!((loaded >> (g + 1)) & 1u)) sees &= 0x0000FFFFu;
+                const uint32_t nan = sh.nan[(it + i) & (2 * kRing - 1)][c0 / 32];
+                const float ca = mt.ks[g] * fac, cb = mt.ks[g + 1] * fac, ea = mt.ve[g], eb = mt.ve[g + 1];
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < kW / 16; ++k) {
-                  const int g = c0 / 16 + k;
-                  const float c = mt.ks[g] * fac, e = mt.ve[g];
-                  const int top = (loaded >> g) & 1u ? hi : -1;
-                  const uint32_t nan = sh.nan[(it + i) & (2 * kRing - 1)][g >> 1] >> (16 * (g & 1));
-                  uint32_t y[16];
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) {
-                    float a = fmaf(t[16 * k + j], c, e);
-                    if ((nan >> j) & 1u) a = __uint_as_float(0x7FC00000u);
-                    a = 16 * k + j <= top && 16 * k + j >= lo ? a : -INFINITY;
-                    mt_ = fmaxf(mt_, a);
-                    y[j] = __float_as_uint(a);
-                  }
-                  tc::tmem_st16(cs + c0 + 16 * k, y);
+                for (int j = 0; j < 32; ++j) {
+                  const float a = fmaf(y[j], j < 16 ? ca : cb, j < 16 ? ea : eb);
+                  y[j] = (sees >> j) & 1u ? a : -INFINITY;
                 }
-                tc::tmem_st_wait();
-              } else {
+                if (nan) {
 #pragma unroll
-                for (int k = 0; k < kW / 16; ++k) {
-                  float a = t[16 * k];
-#pragma unroll
-                  for (int j = 1; j < 15; j += 2) a = fmaxf(fmaxf(a, t[16 * k + j]), t[16 * k + j + 1]);
-                  a = fmaxf(a, t[16 * k + 15]);
-                  mt_ = fmaxf(mt_, fmaf(a, mt.ks[c0 / 16 + k] * fac, mt.ve[c0 / 16 + k]));
+                  for (int j = 0; j < 32; ++j)
+                    if ((nan & sees) >> j & 1u) y[j] = __uint_as_float(0x7FC00000u);
                 }
+                tc::tmem_st16(cs + c0, *(const uint32_t(*)[16])y);
+                tc::tmem_st16(cs + c0 + 16, *(const uint32_t(*)[16])(y + 16));
               }
+              tc::tmem_st_wait();
+            }
+            float t[kPageTile];
+#pragma unroll
+            for (int c0 = 0; c0 < kPageTile; c0 += 32) tc::tmem_ld32(cs + c0, t + c0);
+            tc::tmem_ld_wait();
+            float mt_ = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float a = t[16 * k];
+#pragma unroll
+              for (int j = 1; j < 15; j += 2) a = fmaxf(fmaxf(a, t[16 * k + j]), t[16 * k + j + 1]);
+              a = fmaxf(a, t[16 * k + 15]);
+              mt_ = fmaxf(mt_, masked ? a : fmaf(a, mt.ks[k] * fac, mt.ve[k]));
             }
             const bool grow = mt_ > m + kSlack || (m == -INFINITY && mt_ > m);
             if (__any_sync(0xffffffffu, grow)) {
@@ -626,7 +650,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               if (i > 0) {  // the sums so far (of this piece) follow
                 wait(odone(h), (cnt - 1) & 1);
                 tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 16) {
                   uint32_t v[16];
                   tc::tmem_ld16(co + c0, v);
@@ -638,31 +662,22 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-            for (int c0 = 0; c0 < kPageTile; c0 += kW) {
-              float t[kW];
-              tc::tmem_ld32(cs + c0, t);
-              tc::tmem_ld32(cs + c0 + 32, t + 32);
-              tc::tmem_ld_wait();
-              uint32_t pk[kW / 2];
 #pragma unroll
-              for (int k = 0; k < kW / 16; ++k) {
-                const int g = c0 / 16 + k;
-                const float c = masked ? 1.f : mt.ks[g] * fac, d = (masked ? 0.f : mt.ve[g]) - ref;
-                float sum0 = 0.f, sum1 = 0.f;
+            for (int k = 0; k < 8; ++k) {
+              const float c = masked ? 1.f : mt.ks[k] * fac, d = (masked ? 0.f : mt.ve[k]) - ref;
+              float sum0 = 0.f, sum1 = 0.f;
+              uint32_t pk[8];
 #pragma unroll
-                for (int j = 16 * k; j < 16 * k + 16; j += 2) {
-                  fma2(t[j], t[j + 1], c, d);
-                  t[j] = ex2(t[j]);
-                  t[j + 1] = ex2(t[j + 1]);
-                  add2(sum0, sum1, t[j], t[j + 1]);
-                  pk[j / 2] = half2_bits(t[j], t[j + 1]);
-                }
-                l = fmaf(sum0 + sum1, mt.ive[g], l);
+              for (int j = 0; j < 16; j += 2) {
+                float a0 = t[16 * k + j], a1 = t[16 * k + j + 1];
+                fma2(a0, a1, c, d);
+                a0 = ex2(a0);
+                a1 = ex2(a1);
+                add2(sum0, sum1, a0, a1);
+                pk[j / 2] = half2_bits(a0, a1);
               }
-              // the weights take the place of scores that have been read
-              tc::tmem_st16(cs + c0 / 2, *(const uint32_t(*)[16])pk);
-              tc::tmem_st16(cs + c0 / 2 + 16, *(const uint32_t(*)[16])(pk + 16));
+              l = fmaf(sum0 + sum1, mt.ive[k], l);
+              tc::tmem_st8(cs + 8 * k, pk);  // the weights take the scores' place
             }
             tc::tmem_st_wait();
             tc::fence_before_sync();
@@ -678,32 +693,32 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           const int64_t orow = (int64_t)(sg.row + ti) * s.Hq + sg.u * s.G + rg;
           if (live && !whole) w.ml[prow] = make_float2(m, l);
           const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+          const bool wide = ((uintptr_t)out & 31u) == 0;
+#pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             float v[32];
             tc::tmem_ld32(co + c0, v);
             tc::tmem_ld_wait();
-            if (live) {
-              if (whole) {
-                uint4* dst = (uint4*)(out + orow * D + c0);
+            if (live && whole) {
+              uint32_t y[16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  uint32_t y[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    float a = v[8 * k + 2 * j] * inv, b2 = v[8 * k + 2 * j + 1] * inv;
-                    if (l == 0.f) a = b2 = 0.f;
-                    const __nv_bfloat162 hb = __floats2bfloat162_rn(a, b2);
-                    y[j] = *(const uint32_t*)&hb;
-                  }
-                  dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-              } else {
-                float4* dst = (float4*)(w.acc + prow * D + c0);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat162 hb = __floats2bfloat162_rn(l == 0.f ? 0.f : v[2 * j] * inv,
+                                                               l == 0.f ? 0.f : v[2 * j + 1] * inv);
+                y[j] = *(const uint32_t*)&hb;
               }
+              __nv_bfloat16* dst = out + orow * D + c0;
+              if (wide) {
+                store32(dst, y);
+                store32(dst + 16, y + 8);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  ((uint4*)dst)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+              }
+            } else if (live) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) store32(w.acc + prow * D + c0 + k, (const uint32_t*)v + k);
             }
           }
           tc::fence_before_sync();
@@ -724,13 +739,16 @@ cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t 
   auto kern = page_many_kernel<D>;
   cudaError_t e = ensure_smem(kern, Many<D>::kSmem, done);
   if (e != cudaSuccess) return e;
-  CUtensorMap qm;
-  if (!make_tmap_f16_heads(&qm, w.qrot, s.n_tokens, s.Hq, D, w.tb / 2, s.G)) return cudaErrorInvalidValue;
+  CUtensorMap qm, km, vm;
+  const uint64_t rows = (uint64_t)s.n_pages * s.U * s.T;
+  if (!make_tmap_f16_heads(&qm, w.qrot, s.n_tokens, s.Hq, D, w.tb / 2, s.G) ||
+      !make_tmap_u8_rows(&km, kp, rows, D, s.T) || !make_tmap_u8_rows(&vm, vp, rows, D, s.T))
+    return cudaErrorInvalidValue;
   e = launch_k(page_rotate_kernel<D>, dim3((unsigned)((s.n_tokens + kRotateWarps - 1) / kRotateWarps)),
                dim3(kRotateWarps * 32), 0, stream, true, s, w, (const __nv_bfloat16*)q, q_stride);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(kPageGrid), dim3(kThreads), Many<D>::kSmem, stream, true, s, w, qm,
-                  (const uint8_t*)kp, (const uint8_t*)vp, ks, vs, (__nv_bfloat16*)out);
+  return launch_k(kern, dim3(kPageGrid), dim3(kThreads), Many<D>::kSmem, stream, true, s, w, qm, km, vm,
+                  ks, vs, (__nv_bfloat16*)out);
 }
 
 }  // namespace

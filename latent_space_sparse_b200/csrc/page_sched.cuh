@@ -6,7 +6,9 @@
 // 128-token tiles that any of its rows sees (one tile at least, so that rows
 // that see nothing have somebody to write their zeros).  Tiles are numbered
 // in the order sequence, row block, KV head, tile; CTAs take contiguous
-// ranges of equal length, so no sizes need to be known on the host.  All of
+// ranges of equal length, so no sizes need to be known on the host.  A unit's
+// tiles come after `over` places that stand for what a unit costs besides its
+// tiles (queries, start and end of the pipeline, results).  All of
 // it is integer arithmetic on a sequence's length and number of new tokens.
 #pragma once
 
@@ -49,9 +51,10 @@ SALSC_HD int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
 }
 
 // One sequence's row blocks: n tokens in the cache, the last m of them new (m
-// may exceed n), blocks of tb new tokens, window w (0: none).
+// may exceed n), blocks of tb new tokens, window w (0: none), `over` places
+// before a unit's tiles.
 struct PageBlocks {
-  int n, m, tb, w;
+  int n, m, tb, w, over;
 
   SALSC_HD int count() const { return m / tb + (m % tb != 0); }
   // positions of the first and last row of block k (negative: no position)
@@ -76,13 +79,13 @@ struct PageBlocks {
     if (c < 0) r0 = div_small(-c + tb - 1, tb);
     return r0 < k ? floor_sum(k - r0, kPageTile, tb, c + r0 * tb) : 0;
   }
-  // tiles of blocks 0 .. k-1
+  // places of blocks 0 .. k-1
   SALSC_HD int64_t before(int k) const {
     const int nb = count();
     if (k <= 0) return 0;
-    if (nb == 1) return tiles(0);
+    if (nb == 1) return over + tiles(0);
     const int full = k < nb ? k : nb - 1;
-    int64_t s = ramp((int64_t)n - m + tb - 1, full) + k;
+    int64_t s = ramp((int64_t)n - m + tb - 1, full) + (int64_t)k * (over + 1);
     if (k == nb) s += (n > 1 ? n - 1 : 0) / kPageTile;
     if (w) s -= ramp((int64_t)n - m - w + 1, k);
     return s;

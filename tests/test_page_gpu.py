@@ -219,6 +219,16 @@ def test_attend_strided_queries_of_a_fused_projection():
     check_attend(one, q=fused[:, :8 * s.d].unflatten(1, (8, s.d)))
 
 
+@pytest.mark.parametrize("news", [None, [40, 130]])
+def test_attend_output_at_16_bytes(news):
+    s = Step([300, 140], news)
+    room = torch.full((s.rows * s.hq * s.d + 8,), 7.0, dtype=s.dtype, device=DEV)
+    out = room[8:].view(s.rows, s.hq, s.d)
+    assert out.data_ptr() % 32 == 16
+    s.cache.attend(s.q, *s.pools, out=out)
+    check_attend(s, out)
+
+
 def test_attend_shared_prefix_pages():
     s = Step([200, 200, 170], [5, 1, 90])
     for b in (1, 2):

@@ -21,7 +21,8 @@ int main() {
     const int n = (int)rnd(trial % 3 ? 700 : 40000), m = 1 + (int)rnd(trial % 2 ? 300 : 3000);
     const int tb = 1 + (int)rnd(trial % 5 ? 40 : 256);
     const int w = trial % 4 ? 0 : 1 + (int)rnd(900);
-    const PageBlocks p{n, m, tb, w};
+    const int over = (int)rnd(5);
+    const PageBlocks p{n, m, tb, w, over};
     if (p.count() != (m + tb - 1) / tb) return 1;
     long long before = 0;
     for (int k = 0; k < p.count(); ++k) {
@@ -40,12 +41,12 @@ int main() {
       } else {
         if (p.tile0(k) != first || p.tiles(k) != last - first + 1) return 4;
       }
-      before += p.tiles(k);
+      before += over + p.tiles(k);
     }
     if (p.before(p.count()) != before) return 5;
   }
   // the largest sizes: no 32-bit overflow
-  const PageBlocks big{2147483647, 2147483647, 8, 0};
+  const PageBlocks big{2147483647, 2147483647, 8, 0, 0};
   if (big.tiles(big.count() - 1) != 16777216) return 6;
   long long full = 0;
   for (long long k = 0; k < big.count(); ++k) {
