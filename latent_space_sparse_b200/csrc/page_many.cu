@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kConvert = 128;   // threads of the converting warps
+constexpr int kEarly = 96;     // of a tile's 128 weights: handed on while the others are computed
 constexpr int kRing = 4;        // tiles whose scales are kept
 constexpr float kSlack = 8.f;   // log2 units
 
@@ -65,7 +66,7 @@ struct Shared {
   Segment segments[kSegments];
   TileScales meta[kRing];
   uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
-  uint64_t bars[20 + kSegments];
+  uint64_t bars[22 + kSegments];
   int64_t share[kThreads / 32 + 2];
   uint32_t tmem_base;
 };
@@ -95,12 +96,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ void widen16(const uint4& c, uint32_t (&w)[8]) {
   const uint32_t x[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[i] & 0xFFFFu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[i] >> 16), __NV_E4M3);
-    w[2 * i] = (uint32_t)a.x | ((uint32_t)a.y << 16);
-    w[2 * i + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(w[2 * i]), "=r"(w[2 * i + 1])
+        : "r"(x[i]));
 }
 
 // A byte of w is the NaN code 0x7F or 0xFF.
@@ -113,6 +113,12 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Two fp32 at a time.
@@ -236,6 +242,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   auto sready = [&](int h) { return bar0 + 8u * (8 + h); };
   auto pready = [&](int h) { return bar0 + 8u * (10 + h); };
   auto odone = [&](int h) { return bar0 + 8u * (12 + h); };
+  auto pearly = [&](int h) { return bar0 + 8u * (20 + kSegments + h); };  // the first kEarly weights
   const uint32_t qfull = bar0 + 8u * 14, qfree = bar0 + 8u * 15;
   auto cfull = [&](int v) { return bar0 + 8u * (16 + v); };  // codes of K, of V
   auto cfree = [&](int v) { return bar0 + 8u * (18 + v); };
@@ -250,6 +257,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       tc::mbar_init(sready(i), 2);  // the scores, and the issuer for what it has waited for
       tc::mbar_init(pready(i), 128);
       tc::mbar_init(odone(i), 1);
+      tc::mbar_init(pearly(i), 128);
       tc::mbar_init(cfull(i), 1);
       tc::mbar_init(cfree(i), kConvert);
     }
@@ -273,7 +281,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   const uint32_t tmem = sh.tmem_base;
   bool dead = false;  // a wait gave up: skip the others, so that the kernel ends
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!dead && !tc::mbar_wait(bar, parity, s.flags)) dead = true;
+    if (!dead && !tc::mbar_wait_long(bar, parity, s.flags)) dead = true;
   };
   const int tb2 = w.tb / 2;  // new tokens of a half
 
@@ -311,12 +319,17 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         auto values = [&](int h, int i, bool first) {
           const uint64_t va =
               opaque(tc::sdesc_mnmajor_sw128(sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes, 16384, 1024));
-          wait(pready(h), cnt[h]++ & 1);
+          wait(pearly(h), cnt[h] & 1);
           tc::fence_after_sync();
 #pragma unroll
-          for (int kk = 0; kk < kPageTile / 16; ++kk)
+          for (int kk = 0; kk < kPageTile / 16; ++kk) {
+            if (kk == kEarly / 16) {
+              wait(pready(h), cnt[h]++ & 1);
+              tc::fence_after_sync();
+            }
             tc::mma_f16_ts(tmem + C::kColO + h * D, tmem + h * 128 + kk * 8, va + (kk * 2048 >> 4), id_o,
                            !first || kk > 0);
+          }
           tc::mma_commit(odone(h));
         };
         for (int seg = 0;; ++seg) {
@@ -333,12 +346,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           if (n == 1) tc::mma_commit(qfree);
           for (int i = 0; i < n; ++i, ++it) {
             wait(vfull(it & 1), (it >> 1) & 1);
+            if (i + 1 < n) wait(kfull((it + 1) & 1), ((it + 1) >> 1) & 1);
             values(0, it, i == 0);
-            if (i + 1 < n) {
-              wait(kfull((it + 1) & 1), ((it + 1) >> 1) & 1);
-              tc::fence_after_sync();
-              scores(0, it + 1);
-            }
+            if (i + 1 < n) scores(0, it + 1);
             if (two) values(1, it, i == 0);
             tc::mma_commit(vfree(it & 1));
             if (i + 1 < n) {
@@ -490,6 +500,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           uint32_t(&nan)[4] = sh.nan[it & (2 * kRing - 1)];
           wait(cfull(0), it & 1);
           const uint32_t loaded = mt.loaded;
+          const bool plain = mt.plain;
           const bool full = tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu;
           // codes of pass j; zeros for tokens that no row sees
           auto codes = [&](int v, int j) {
@@ -548,7 +559,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               const int rr = row_of(j + k);
               uint32_t x[8];
               widen16(c[k], x);
-              if (!mt.plain) {
+              if (!plain) {
                 const uint32_t f = mt.vf[rr >> 4];
 #pragma unroll
                 for (int i2 = 0; i2 < 8; ++i2) {
@@ -633,15 +644,19 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
 #pragma unroll
             for (int c0 = 0; c0 < kPageTile; c0 += 32) tc::tmem_ld32(cs + c0, t + c0);
             tc::tmem_ld_wait();
-            float mt_ = -INFINITY;
+            // eight chains side by side: one alone would wait for each of its steps
+            float a[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float a = t[16 * k];
+            for (int k = 0; k < 8; ++k) a[k] = fmaxf(t[16 * k], t[16 * k + 1]);
 #pragma unroll
-              for (int j = 1; j < 15; j += 2) a = fmaxf(fmaxf(a, t[16 * k + j]), t[16 * k + j + 1]);
-              a = fmaxf(a, t[16 * k + 15]);
-              mt_ = fmaxf(mt_, masked ? a : fmaf(a, mt.ks[k] * fac, mt.ve[k]));
+            for (int j = 2; j < 16; j += 2)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) a[k] = max3(a[k], t[16 * k + j], t[16 * k + j + 1]);
+            if (!masked) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) a[k] = fmaf(a[k], mt.ks[k] * fac, mt.ve[k]);
             }
+            const float mt_ = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
             const bool grow = mt_ > m + kSlack || (m == -INFINITY && mt_ > m);
             if (__any_sync(0xffffffffu, grow)) {
               const float al = grow ? ex2(m - mt_) : 1.f;  // 0 from m = -inf
@@ -678,6 +693,11 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               }
               l = fmaf(sum0 + sum1, mt.ive[k], l);
               tc::tmem_st8(cs + 8 * k, pk);  // the weights take the scores' place
+              if (k == kEarly / 16 - 1) {
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                tc::mbar_arrive(pearly(h));
+              }
             }
             tc::tmem_st_wait();
             tc::fence_before_sync();

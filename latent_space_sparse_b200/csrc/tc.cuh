@@ -88,6 +88,29 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
   return mbar_wait_limit(bar, parity, flags, kWaitLimitNs);
 }
 
+// mbar_wait for long waits: a try may sleep up to 20 us, and takes that many fewer issue slots
+// from the warps that work.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint32_t* flags) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      if (flags) atomicOr(flags, FLAG_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- TMA
 
 // 2-D tiled load of one box into shared memory, completing on `bar`.
