@@ -295,30 +295,27 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       // ------------------------------------------------ MMA issuer
-      if (warp == 12 && tc::elect_one()) {
+      // All lanes run it, so that the compiler sees that descriptors and addresses
+      // are the warp's and keeps them in uniform registers; one lane issues.
+      if (warp == 12) {
+        const uint32_t lead = tc::elect_one();
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, kPageTile, false);
         constexpr uint32_t id_o = tc::idesc_f16_f32(128, D, true);
         int cnt[2] = {0, 0};
-        // descriptors are formed from opaque starts, so that the compiler does not
-        // keep one for every step in registers
-        auto opaque = [](uint64_t d) {
-          asm volatile("" : "+l"(d));
-          return d;
-        };
         auto scores = [&](int h, int i) {
-          const uint64_t qa = opaque(tc::sdesc_kmajor_sw128(sm0 + (uint32_t)h * C::kQHalf));
-          const uint64_t ka = opaque(tc::sdesc_kmajor_sw128(sm0 + C::kOffK + (uint32_t)(i & 1) * C::kTileBytes));
+          const uint64_t qa = tc::sdesc_kmajor_sw128(sm0 + (uint32_t)h * C::kQHalf);
+          const uint64_t ka = tc::sdesc_kmajor_sw128(sm0 + C::kOffK + (uint32_t)(i & 1) * C::kTileBytes);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (uint64_t)((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-            tc::mma_bf16(tmem + h * 128, qa + off, ka + off, id_s, kk > 0);
+            tc::mma_lead(lead, tmem + h * 128, qa + off, ka + off, id_s, kk > 0);
           }
-          tc::mma_commit(sready(h));
-          tc::mbar_arrive(sready(h));
+          tc::commit_lead(lead, sready(h));
+          if (lead) tc::mbar_arrive(sready(h));
         };
         auto values = [&](int h, int i, bool first) {
           const uint64_t va =
-              opaque(tc::sdesc_mnmajor_sw128(sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes, 16384, 1024));
+              tc::sdesc_mnmajor_sw128(sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes, 16384, 1024);
           wait(pearly(h), cnt[h] & 1);
           tc::fence_after_sync();
 #pragma unroll
@@ -327,34 +324,34 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               wait(pready(h), cnt[h]++ & 1);
               tc::fence_after_sync();
             }
-            tc::mma_f16_ts(tmem + C::kColO + h * D, tmem + h * 128 + kk * 8, va + (kk * 2048 >> 4), id_o,
+            tc::mma_ts_lead(lead, tmem + C::kColO + h * D, tmem + h * 128 + kk * 8, va + (kk * 2048 >> 4), id_o,
                            !first || kk > 0);
           }
-          tc::mma_commit(odone(h));
+          tc::commit_lead(lead, odone(h));
         };
         for (int seg = 0;; ++seg) {
           const Segment& sg = segment(seg);
-          const int n = dead ? 0 : sg.n;
+          const int n = __shfl_sync(0xffffffffu, dead ? 0 : sg.n, 0);
           if (n == 0) break;
-          const bool two = sg.p1 - sg.p0 >= tb2;
+          const bool two = __shfl_sync(0xffffffffu, sg.p1 - sg.p0, 0) >= tb2;
           wait(qfull, seg & 1);
           wait(kfull(it & 1), (it >> 1) & 1);
           tc::fence_after_sync();
           scores(0, it);
           if (two) scores(1, it);
-          tc::mma_commit(kfree(it & 1));
-          if (n == 1) tc::mma_commit(qfree);
+          tc::commit_lead(lead, kfree(it & 1));
+          if (n == 1) tc::commit_lead(lead, qfree);
           for (int i = 0; i < n; ++i, ++it) {
             wait(vfull(it & 1), (it >> 1) & 1);
             if (i + 1 < n) wait(kfull((it + 1) & 1), ((it + 1) >> 1) & 1);
             values(0, it, i == 0);
             if (i + 1 < n) scores(0, it + 1);
             if (two) values(1, it, i == 0);
-            tc::mma_commit(vfree(it & 1));
+            tc::commit_lead(lead, vfree(it & 1));
             if (i + 1 < n) {
               if (two) scores(1, it + 1);
-              tc::mma_commit(kfree((it + 1) & 1));
-              if (i + 2 == n) tc::mma_commit(qfree);
+              tc::commit_lead(lead, kfree((it + 1) & 1));
+              if (i + 2 == n) tc::commit_lead(lead, qfree);
             }
           }
         }
@@ -473,103 +470,108 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       // rows, and eight lanes that access shared memory together those of rows
       // p and p ^ 5: the swizzles then send them to all banks, both for reading
       // (rows that differ in bit 2) and for writing (in bit 0).
+      constexpr int kWarpC = 8;  // the first of these warps
+      const int ct = tid - kWarpC * 32;
       constexpr int kHalves = D / 64;
-      constexpr int kPass = 4 * kHalves;
       constexpr int kBatch = 4;  // passes whose codes are read together
-      const int ct = tid - 256;
-      const int row = (warp - 8) * 8 + ((lane >> 3) ^ ((lane >> 2 & 1) * 5));
-      auto row_of = [&](int j) { return j / kHalves * 32 + row; };
-      auto col_of = [&](int j) { return j % kHalves * 4 + (lane & 3); };
+      const int row = (warp - kWarpC) * 8 + ((lane >> 3) ^ ((lane >> 2 & 1) * 5)), col = lane & 3;
+      // this thread's chunk of codes of a pass, and its two chunks of f16
+      const uint32_t in0 = C::kOffCodes + row * D + ((col ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4);
+      const uint32_t in1 = in0 ^ 64;  // d = 128: of the second half of the row
+      const uint32_t out0 = row * 128 + (((2 * col) ^ (row & 7)) << 4), out1 = out0 ^ 16;
+      auto put = [&](uint32_t off, const uint32_t (&x)[8]) {
+        *(uint4*)(smem + off + out0) = make_uint4(x[0], x[1], x[2], x[3]);
+        *(uint4*)(smem + off + out1) = make_uint4(x[4], x[5], x[6], x[7]);
+      };
+      // a tile that all rows see whole and whose f are 1
+      auto convert = [&](uint32_t in, uint32_t out) {
+#pragma unroll 1
+        for (int a = 0; a < kHalves; ++a) {
+          uint4 c[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            c[k] = *(const uint4*)(smem + in + (k % kHalves ? in1 : in0) + k / kHalves * 32 * D);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            uint32_t x[8];
+            widen16(c[k], x);
+            put(out + k % kHalves * 16384 + k / kHalves * 4096, x);
+          }
+          in += kBatch / kHalves * 32 * D;
+          out += kBatch / kHalves * 4096;
+        }
+      };
+      // any tile
+      auto convert_any = [&](uint32_t in, uint32_t out, bool full, int64_t tile0, int lo, int p1, bool values,
+                             const TileScales& mt, uint32_t* nan) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < kPageTile; r0 += 32) {
+          const int rr = r0 + row;
+          uint4 c[kHalves];
+          bool bad = false;
+#pragma unroll
+          for (int k = 0; k < kHalves; ++k) {
+            c[k] = *(const uint4*)(smem + in + (k ? in1 : in0) + r0 * D);
+            bad |= has_nan(c[k].x) || has_nan(c[k].y) || has_nan(c[k].z) || has_nan(c[k].w);
+          }
+          if (!full) {
+            // Rows differ in what they see.  A NaN would not be hidden by a
+            // weight of zero: such a token's values become zeros, and the NaN is
+            // handed to the rows that see it by their weights.
+            const int64_t tok = tile0 + rr;
+            const bool none = tok < lo || tok > p1 || !((mt.loaded >> (rr >> 4)) & 1u);
+            const uint32_t any = __ballot_sync(0xffffffffu, bad && !none) >> (lane & 28) & 15u;  // the row's lanes
+            if (none || (values && any))
+#pragma unroll
+              for (int k = 0; k < kHalves; ++k) c[k] = make_uint4(0, 0, 0, 0);
+            if (values && any && col == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
+          }
+          const uint32_t f = mt.vf[rr >> 4];
+#pragma unroll
+          for (int k = 0; k < kHalves; ++k) {
+            uint32_t x[8];
+            widen16(c[k], x);
+            if (values) {
+#pragma unroll
+              for (int a = 0; a < 8; ++a) {
+                const __half2 y = __hmul2(*(const __half2*)&x[a], *(const __half2*)&f);
+                x[a] = *(const uint32_t*)&y;
+              }
+            }
+            put(out + k * 16384 + r0 * 128, x);
+          }
+        }
+      };
       for (int seg = 0;; ++seg) {
         const Segment& sg = segment(seg);
         const int n = dead ? 0 : sg.n;
         if (n == 0) break;
         const int p0 = sg.p0, p1 = sg.p1, lo = sg.lo, all_lo = sg.all_lo;
         const int64_t first = (int64_t)sg.t0 * kPageTile;
-        // f16 rows into a swizzled tile: blocks of 64 elements (128 bytes) by row
-        auto store = [&](uint32_t tile, int rr, int c, const uint32_t (&x)[8]) {
-          unsigned char* base = smem + tile + (c >> 2) * 16384 + rr * 128;
-          const int k = c * 2 & 7;
-          *(uint4*)(base + ((k ^ (rr & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          *(uint4*)(base + (((k + 1) ^ (rr & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-        };
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it & 1;
           const int64_t tile0 = first + (int64_t)i * kPageTile;
           const TileScales& mt = meta[it & (kRing - 1)];
           uint32_t(&nan)[4] = sh.nan[it & (2 * kRing - 1)];
           wait(cfull(0), it & 1);
-          const uint32_t loaded = mt.loaded;
+          const bool full = tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && mt.loaded == 0xFFu;
           const bool plain = mt.plain;
-          const bool full = tile0 >= all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu;
-          // codes of pass j; zeros for tokens that no row sees
-          auto codes = [&](int v, int j) {
-            const int rr = row_of(j), cc = col_of(j);
-            const int64_t tok = tile0 + rr;
-            uint4 c = *(const uint4*)(smem + C::kOffCodes + v * C::kCodeBytes + rr * D +
-                                      ((cc ^ (D == 128 ? rr & 7 : rr >> 1 & 3)) << 4));
-            if (!full && (tok < lo || tok > p1 || !((loaded >> (rr >> 4)) & 1u))) c = make_uint4(0, 0, 0, 0);
-            return c;
-          };
           wait(kfree(st), ((it >> 1) & 1) ^ 1);
           // a later tile's; all have left the slot's last one, and none is there yet
           if (ct < 4) sh.nan[(it + 2) & (2 * kRing - 1)][ct] = 0;
-#pragma unroll 1
-          for (int j = 0; j < kPass; j += kBatch) {
-            uint4 c[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) c[k] = codes(0, j + k);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              uint32_t x[8];
-              widen16(c[k], x);
-              store(C::kOffK + st * C::kTileBytes, row_of(j + k), col_of(j + k), x);
-            }
-          }
+          if (full)
+            convert(0, C::kOffK + st * C::kTileBytes);
+          else
+            convert_any(0, C::kOffK + st * C::kTileBytes, false, tile0, lo, p1, false, mt, nan);
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(cfree(0));
           tc::mbar_arrive(kfull(st));
           wait(cfull(1), it & 1);
           wait(vfree(st), ((it >> 1) & 1) ^ 1);
-#pragma unroll 1
-          for (int j = 0; j < kPass; j += kBatch) {
-            uint4 c[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) c[k] = codes(1, j + k);
-            if (!full) {
-              // Rows differ in what they see.  A NaN would not be hidden by a
-              // weight of zero: such a token's values become zeros, and the NaN is
-              // handed to the rows that see it by their weights.
-#pragma unroll
-              for (int k = 0; k < kBatch; k += kHalves) {
-                bool bad = false;
-#pragma unroll
-                for (int a = k; a < k + kHalves; ++a)
-                  bad |= has_nan(c[a].x) || has_nan(c[a].y) || has_nan(c[a].z) || has_nan(c[a].w);
-                if (__ballot_sync(0xffffffffu, bad) >> (lane & 28) & 15u) {  // the row's lanes
-#pragma unroll
-                  for (int a = k; a < k + kHalves; ++a) c[a] = make_uint4(0, 0, 0, 0);
-                  const int rr = row_of(j + k);
-                  if ((lane & 3) == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
-                }
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int rr = row_of(j + k);
-              uint32_t x[8];
-              widen16(c[k], x);
-              if (!plain) {
-                const uint32_t f = mt.vf[rr >> 4];
-#pragma unroll
-                for (int i2 = 0; i2 < 8; ++i2) {
-                  const __half2 y = __hmul2(*(const __half2*)&x[i2], *(const __half2*)&f);
-                  x[i2] = *(const uint32_t*)&y;
-                }
-              }
-              store(C::kOffV + st * C::kTileBytes, rr, col_of(j + k), x);
-            }
-          }
+          if (full && plain)
+            convert(C::kCodeBytes, C::kOffV + st * C::kTileBytes);
+          else
+            convert_any(C::kCodeBytes, C::kOffV + st * C::kTileBytes, full, tile0, lo, p1, true, mt, nan);
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(cfree(1));
           tc::mbar_arrive(vfull(st));
