@@ -18,6 +18,7 @@ constexpr int kPageMaxHeadDim = 128;
 // rotation's frequencies: passed to the kernels by value.
 struct PageStep {
   int B, Hq, U, G, d, T;  // batch, query heads, KV heads, heads per KV head, head dim, page size
+  int log_t;              // T = 2^log_t
   int n_pages, max_pages, n_tokens, max_q;
   int window;  // 0: none
   int rotate;  // 0: keys and queries are taken as they are
@@ -26,8 +27,8 @@ struct PageStep {
   const int32_t* lens;
   const int32_t* offs;  // null: row b is sequence b's one token
   uint32_t* flags;
-  // frequency of pair i in turns per position: base^(-2i/d) / 2pi
-  double turns[kPageMaxHeadDim / 2];
+  // frequency of pair i in turns per position, base^(-2i/d) / 2pi, in units of 2^-64
+  uint64_t turns[kPageMaxHeadDim / 2];
 };
 
 // One sequence's part of a step, cut to the step's bounds.
@@ -75,50 +76,59 @@ __device__ __forceinline__ int page_of(const PageStep& s, int b, int j) {
   return -1;
 }
 
-// Block-wide: item x of a list in which sequence b has count(b) items; the
-// sequence (-1 when x is past the end) and the item's index in it.  `sm`: 34
-// ints of shared memory.  Every thread calls it, with the same x.
-template <typename F>
-__device__ __forceinline__ void page_find(int B, int x, int* sm, F count, int& b_out, int& r_out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  if (tid == 0) sm[32] = -1;
-  int left = x;
-  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
-    const int b = b0 + tid;
-    const int c = b < B ? count(b) : 0;
-    int inc = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) sm[warp] = inc;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += sm[w];
-      total += sm[w];
-    }
-    const int end = before + inc;
-    if (left >= end - c && left < end) {
-      sm[32] = b;
-      sm[33] = left - (end - c);
-    }
-    __syncthreads();
-    if (left < total) break;
-    left -= total;
-  }
-  __syncthreads();
-  b_out = sm[32];
-  r_out = sm[33];
+// Two fp32 at a time.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float m, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
 }
 
-// cos and sin of position pos at `turns` turns per position: the angle is
-// formed and reduced to half a turn in fp64, so that far positions keep fp32's
-// accuracy.
-__device__ __forceinline__ void page_cs(int pos, double turns, float& c, float& s) {
-  const double a = (double)pos * turns;
-  sincospif((float)(2.0 * (a - rint(a))), &s, &c);
+__device__ __forceinline__ void mul2(float& a0, float& a1, float m) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(m));
+}
+
+// Item x of a list in which sequence b has count(b) items: the sequence (-1 when
+// x is past the end) and the item's index in it.  Every warp finds it for
+// itself, without a barrier; all lanes call it, with the same x.
+template <typename F>
+__device__ __forceinline__ void page_find(int B, int x, F count, int& b_out, int& r_out) {
+  const int lane = threadIdx.x & 31;
+  b_out = -1;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int c = b0 + lane < B ? count(b0 + lane) : 0;
+    int end = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += t;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, x < end);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      b_out = b0 + l;
+      r_out = x - __shfl_sync(0xffffffffu, end - c, l);
+      return;
+    }
+    x -= __shfl_sync(0xffffffffu, end, 31);
+  }
+}
+
+// cos and sin of position pos at `turns` (of 2^64) turns per position: the
+// product's low 64 bits are the angle in parts of a turn, exact to 2^-33 of a
+// turn at every position below 2^31, so that far positions keep fp32's accuracy.
+__device__ __forceinline__ void page_cs(int pos, uint64_t turns, float& c, float& s) {
+  const int32_t a = (int32_t)(((uint64_t)(uint32_t)pos * turns) >> 32);
+  sincospif((float)a * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
 }
 
 // ---------------------------------------------------------------- attention

@@ -40,6 +40,7 @@ salsc_status make_step(const salsc_page_desc* D, salsc::PageStep* S) {
   s.G = s.Hq / s.U;
   s.d = D->head_dim;
   s.T = D->page_size;
+  while ((1 << s.log_t) < s.T) ++s.log_t;
   s.n_pages = D->n_pages;
   s.max_pages = D->max_pages;
   s.n_tokens = D->n_tokens;
@@ -51,12 +52,10 @@ salsc_status make_step(const salsc_page_desc* D, salsc::PageStep* S) {
   s.lens = D->seq_lens_dev;
   s.offs = D->q_offsets_dev;
   if (s.rotate) {
-    // one pow for each eight frequencies, products between them (a few ulp of
-    // fp64, below 1e-5 turns at position 2^31)
-    const double step = pow(D->rope_base, -2.0 / s.d);
-    for (int i = 0; i < s.d / 2; ++i)
-      s.turns[i] = i % 8 ? s.turns[i - 1] * step
-                         : pow(D->rope_base, -2.0 * i / s.d) * 0.15915494309189533577;
+    // products of the first power: 64 roundings of a 64-bit mantissa
+    const long double step = powl((long double)D->rope_base, -2.0L / s.d);
+    long double f = 0.159154943091895335768883763372514362L;
+    for (int i = 0; i < s.d / 2; ++i, f *= step) s.turns[i] = (uint64_t)(f * 18446744073709551616.0L + 0.5L);
   }
   *S = s;
   return SALSC_OK;

@@ -20,16 +20,19 @@
 // 32 elements a thread held in registers between the maximum and the codes.
 // A thread's 16-element chunks are 8 elements of either half of a row, so a
 // rotated pair is one thread's and global accesses are 16-byte loads and
-// 8-byte stores.  A CTA takes one page and every gridDim.y-th group of its
-// items, so that the cos/sin table of the page's positions is computed once
-// per CTA and not once per head.
+// 8-byte stores.  A CTA takes some items of one page; how many is a balance:
+// cos and sin of the page's positions are computed once per CTA, and few items
+// to a CTA keep more loads in flight, with the loads issued before cos and sin
+// are computed.
+#include <algorithm>
+
 #include "page.cuh"
 
 namespace salsc {
 namespace {
 
 constexpr int kMinExp = -100;  // exponent of the scale of a page that holds only zeros
-constexpr int kTargetCtas = 2 * 148;
+constexpr int kTargetCtas = 8 * 148;  // small steps: CTAs that run at once
 
 // The least 2^e >= a / 448, e >= kMinExp (a finite, >= 0).  448 = 1.75 * 2^8.
 __device__ __forceinline__ float pow2_scale(float a) {
@@ -40,15 +43,33 @@ __device__ __forceinline__ float pow2_scale(float a) {
 }
 
 __device__ __forceinline__ float finite_or_zero(float x) { return fabsf(x) <= 3.402823466e38f ? fabsf(x) : 0.f; }
-
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *(const uint4*)p;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldg((const uint4*)p + i);
+  return r;
+}
+__device__ __forceinline__ void widen8(const Raw8<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.v[i].x), x[4 * i + 1] = __uint_as_float(r.v[i].y);
+    x[4 * i + 2] = __uint_as_float(r.v[i].z), x[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+__device__ __forceinline__ void widen8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
@@ -56,13 +77,64 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
+// The larger of a and the elements' sizes; NaN if one of them is.
+__device__ __forceinline__ float max_size(const Raw8<float>& r, float a) {
+  float x[8];
+  widen8(r, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(x[i]));
+  return a;
+}
+__device__ __forceinline__ float max_size(const Raw8<__nv_bfloat16>& r, float a) {
+  auto two = [](uint32_t w) { return __habs2(*(const __nv_bfloat162*)&w); };
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(two(r.v[0].x), two(r.v[0].y)),
+                                       __hmax2_nan(two(r.v[0].z), two(r.v[0].w)));
+  return max_nan(a, max_nan(__low2float(m), __high2float(m)));
+}
+// The larger of a and the sums of sizes of pairs.
+template <typename T>
+__device__ __forceinline__ float max_pair(const Raw8<T>& r0, const Raw8<T>& r1, float a) {
+  float x[8], y[8];
+  widen8(r0, x);
+  widen8(r1, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(x[i]) + fabsf(y[i]));
+  return a;
+}
+// The same for any values: what is not finite does not count.
+template <typename T>
+__device__ __noinline__ float max_finite(const Raw8<T> r0, const Raw8<T> r1, bool pairs) {
+  float x[8], y[8], a = 0.f;
+  widen8(r0, x);
+  widen8(r1, y);
+  for (int i = 0; i < 8; ++i) {
+    const float x0 = finite_or_zero(x[i]), y0 = finite_or_zero(y[i]);
+    a = fmaxf(a, pairs ? fminf(x0 + y0, 3.402823466e38f) : fmaxf(x0, y0));
+  }
+  return a;
+}
+
+__device__ __forceinline__ uint2 codes8(float (&x)[8], float inv) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE,
-                                    __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    mul2(x[2 * i], x[2 * i + 1], inv);
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// Two pairs (a, b) rotated.
+__device__ __forceinline__ void turn2(float& a0, float& a1, float& b0, float& b1, float c0, float c1,
+                                      float s0, float s1) {
+  asm("{\n\t.reg .b64 a, b, c, s, m, n, p, q;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+      "mov.b64 s, {%6, %7};\n\tmov.b64 n, {%8, %9};\n\t"
+      "mul.rn.f32x2 m, a, c;\n\tfma.rn.f32x2 m, b, n, m;\n\t"
+      "mul.rn.f32x2 p, b, c;\n\tfma.rn.f32x2 p, a, s, p;\n\t"
+      "mov.b64 {%0, %1}, m;\n\tmov.b64 {%2, %3}, p;\n\t}"
+      : "+f"(a0), "+f"(a1), "+f"(b0), "+f"(b1)
+      : "f"(c0), "f"(c1), "f"(s0), "f"(s1), "f"(-s0), "f"(-s1));
 }
 
 __device__ __forceinline__ uint2 recode8(uint2 v, float ratio) {
@@ -80,16 +152,15 @@ __device__ __forceinline__ uint2 recode8(uint2 v, float ratio) {
 }
 
 // D: head dim.  Block of 256 threads (512 for T * D = 16384); grid (touched
-// pages at most, head parts).
+// pages at most, parts of a page's items).
 template <typename T, int D, int kThreads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 1024 : 768) / kThreads)
 page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, int64_t k_stride,
                    const T* __restrict__ V, int64_t v_stride, uint8_t* __restrict__ k_pages,
                    uint8_t* __restrict__ v_pages, float* __restrict__ k_scales,
                    float* __restrict__ v_scales) {
-  extern __shared__ float2 cs[];  // [T][D/2] cos, sin of the new tokens' slots
-  __shared__ int find[34];
-  __shared__ float red[kThreads / 32];
+  extern __shared__ __align__(16) float cs[];  // [T][D/2] cos of the new tokens' slots, [T][D/2] sin
+  __shared__ float red[2][kThreads / 32];
   constexpr int kHalf = D / 2;
   constexpr int kRowChunks = D / 16;  // 16-element chunks of a row
   const int tid = threadIdx.x;
@@ -97,80 +168,99 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
   allow_dependent_launch();
 
   // the x-th touched page of the step
-  int b, j;
-  page_find(s.B, blockIdx.x, find, [&](int i) {
+  int b, j = 0;
+  page_find(s.B, blockIdx.x, [&](int i) {
     const PageSeq q = page_seq(s, i);
     const int m = min(q.m, q.n);
-    return m > 0 ? (q.n - 1) / s.T - (q.n - m) / s.T + 1 : 0;
+    return m > 0 ? ((q.n - 1) >> s.log_t) - ((q.n - m) >> s.log_t) + 1 : 0;
   }, b, j);
   if (b < 0) return;
   const PageSeq q = page_seq(s, b);
   const int m = min(q.m, q.n), start = q.n - m;
-  j += start / s.T;
+  j += start >> s.log_t;
   const int pg = page_of(s, b, j);
   if (pg < 0) return;
   const int lo = max(start - j * s.T, 0), hi = min(q.n - j * s.T, s.T);  // new slots
   // row of slot 0 (may lie before the first new row)
   const int64_t row0 = (int64_t)q.row0 + (q.m - m) + ((int64_t)j * s.T - start);
 
-  if (s.rotate) {
-    for (int e = tid; e < (hi - lo) * kHalf; e += kThreads) {
-      const int slot = lo + e / kHalf, i = e % kHalf;
-      float c, sn;
-      page_cs(j * s.T + slot, s.turns[i], c, sn);
-      cs[slot * kHalf + i] = make_float2(c, sn);
-    }
-  }
-  __syncthreads();
-
-  const int per = s.T * D / 32;       // threads of an item
-  const int items = kThreads / per;   // items of a pass
-  const int ti = tid % per, warps = per / 32;
-  for (int it0 = blockIdx.y * items; it0 < 2 * s.U; it0 += gridDim.y * items) {
-    const int it = it0 + tid / per;
+  constexpr int kLogD = D == 128 ? 7 : 6;
+  const int log_per = s.log_t + kLogD - 5, per = 1 << log_per;  // threads of an item
+  const int items = kThreads >> log_per;                        // items of a pass
+  const int ti = tid & (per - 1), warps = per >> 5;
+  // this part's items, keys first, then values
+  const int passes = (2 * s.U + items - 1) / items;
+  const int first = (int)((int64_t)blockIdx.y * passes / gridDim.y);
+  const int last = (int)((int64_t)(blockIdx.y + 1) * passes / gridDim.y);
+  for (int pass = first; pass < last; ++pass) {
+    const int it = pass * items + (tid >> log_per);
     const bool live = it < 2 * s.U;
-    const bool val = it >= s.U;  // keys first, then values
+    const bool val = it >= s.U;
     const int u = val ? it - s.U : it;
     const T* X = val ? V : K;
     const int64_t stride = val ? v_stride : k_stride;
     const bool turn = s.rotate && !val;
-    float x[2][2][8];
-    float a = 0.f;
+    float* scales = (val ? v_scales : k_scales) + (size_t)pg * s.U + u;
+    uint8_t* page = (val ? v_pages : k_pages) + ((size_t)pg * s.U + u) * s.T * D;
+    Raw8<T> x[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int ch = ti + k * per, slot = ch / kRowChunks, i0 = ch % kRowChunks * 8;
       if (live && slot >= lo && slot < hi) {
         const T* p = X + (row0 + slot) * stride + u * D + i0;
-        load8(p, x[k][0]);
-        load8(p + kHalf, x[k][1]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a0 = finite_or_zero(x[k][0][i]), a1 = finite_or_zero(x[k][1][i]);
-          a = fmaxf(a, turn ? fminf(__fadd_rn(a0, a1), 3.402823466e38f) : fmaxf(a0, a1));
+        x[k][0] = load8(p);
+        x[k][1] = load8(p + kHalf);
+      }
+    }
+    float old = 0.f;
+    if (live && lo > 0) old = *scales;
+    if (pass == first) {
+      // with the first loads in flight
+      if (s.rotate && pass * items < s.U) {
+        for (int e = tid; e < (hi - lo) * kHalf; e += kThreads) {
+          const int slot = lo + e / kHalf, i = e % kHalf;
+          float c, sn;
+          page_cs(j * s.T + slot, s.turns[i], c, sn);
+          cs[slot * kHalf + i] = c;
+          cs[(s.T + slot) * kHalf + i] = sn;
         }
+      }
+      __syncthreads();
+    }
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int slot = (ti + k * per) / kRowChunks;
+      if (live && slot >= lo && slot < hi)
+        a = turn ? max_pair(x[k][0], x[k][1], a) : max_size(x[k][1], max_size(x[k][0], a));
+    }
+    if (!(a <= 3.402823466e38f)) {
+      a = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int slot = (ti + k * per) / kRowChunks;
+        if (live && slot >= lo && slot < hi) a = fmaxf(a, max_finite(x[k][0], x[k][1], turn));
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    // the item's threads meet; each has read the old scale before one of them writes it
     if (warps > 1) {
-      if ((tid & 31) == 0) red[tid >> 5] = a;
-      __syncthreads();
-      const int w0 = (tid >> 5) / warps * warps;
-      for (int w = 0; w < warps; ++w) a = fmaxf(a, red[w0 + w]);
-      __syncthreads();
+      float* r = red[pass & 1];
+      if ((tid & 31) == 0) r[tid >> 5] = a;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + (tid >> log_per)), "r"(per) : "memory");
+      const int w0 = (tid >> 5) & -warps;
+      for (int w = 0; w < warps; ++w) a = fmaxf(a, r[w0 + w]);
+    } else {
+      __syncwarp();
     }
     if (!live) continue;
-    float* scales = (val ? v_scales : k_scales) + (size_t)pg * s.U + u;
-    uint8_t* page = (val ? v_pages : k_pages) + ((size_t)pg * s.U + u) * s.T * D;
     float sc = pow2_scale(a), ratio = 1.f;
-    if (lo > 0) {
-      const float old = *scales;
-      if (old > 0.f && old <= 3.402823466e38f) {
-        ratio = old / sc;
-        if (ratio >= 1.f) {
-          sc = old;
-          ratio = 1.f;
-        }
+    if (old > 0.f && old <= 3.402823466e38f) {
+      ratio = old / sc;
+      if (ratio >= 1.f) {
+        sc = old;
+        ratio = 1.f;
       }
     }
     const float inv = 1.f / sc;
@@ -179,27 +269,25 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
       const int ch = ti + k * per, slot = ch / kRowChunks, i0 = ch % kRowChunks * 8;
       uint8_t* row = page + slot * D + i0;
       if (slot >= lo && slot < hi) {
+        float y[2][8];
+        widen8(x[k][0], y[0]);
+        widen8(x[k][1], y[1]);
         if (turn) {
+          const float* c = cs + slot * kHalf + i0;
+          const float* sn = c + s.T * kHalf;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 r = cs[slot * kHalf + i0 + i];
-            const float x0 = x[k][0][i], x1 = x[k][1][i];
-            x[k][0][i] = x0 * r.x - x1 * r.y;
-            x[k][1][i] = x1 * r.x + x0 * r.y;
+          for (int i = 0; i < 8; i += 4) {
+            const float4 c4 = *(const float4*)(c + i), s4 = *(const float4*)(sn + i);
+            turn2(y[0][i], y[0][i + 1], y[1][i], y[1][i + 1], c4.x, c4.y, s4.x, s4.y);
+            turn2(y[0][i + 2], y[0][i + 3], y[1][i + 2], y[1][i + 3], c4.z, c4.w, s4.z, s4.w);
           }
         }
-        *(uint2*)row = codes8(x[k][0], inv);
-        *(uint2*)(row + kHalf) = codes8(x[k][1], inv);
+        *(uint2*)row = codes8(y[0], inv);
+        *(uint2*)(row + kHalf) = codes8(y[1], inv);
       } else if (slot < lo && ratio != 1.f) {
         *(uint2*)row = recode8(*(const uint2*)row, ratio);
         *(uint2*)(row + kHalf) = recode8(*(const uint2*)(row + kHalf), ratio);
       }
-    }
-    // every thread of the item has read the old scale before one of them writes it
-    if (warps > 1) {
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + tid / per), "r"(per) : "memory");
-    } else {
-      __syncwarp();
     }
     if (ti == 0) *scales = sc;
   }
@@ -211,7 +299,7 @@ cudaError_t launch(const PageStep& s, const void* K, int64_t k_stride, const voi
                    float* v_scales, cudaStream_t stream) {
   static int done[kMaxDevices];
   auto kern = page_append_kernel<T, D, kThreads>;
-  const size_t smem = sizeof(float2) * s.T * (D / 2);
+  const size_t smem = 2 * sizeof(float) * s.T * (D / 2);
   const cudaError_t e = ensure_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   // a sequence with m new tokens touches at most floor((m + T - 2) / T) + 1 <= m pages
@@ -220,9 +308,11 @@ cudaError_t launch(const PageStep& s, const void* K, int64_t k_stride, const voi
     pages = (int64_t)s.n_tokens / s.T + 2 * (int64_t)s.B;
     if (pages > s.n_tokens) pages = s.n_tokens;
   }
-  const int per = s.T * D / 32, passes = (2 * s.U * per + kThreads - 1) / kThreads;
-  int64_t parts = (kTargetCtas + pages - 1) / pages;
-  if (parts > passes) parts = passes;
+  const int per = s.T * D / 32, items = kThreads / per, passes = (2 * s.U + items - 1) / items;
+  // passes of a CTA: so many that it computes up to four cos and sin a thread for each
+  int64_t parts = passes / std::max(1, s.T * (D / 2) / kThreads / 4);
+  parts = std::max(parts, (kTargetCtas + pages - 1) / pages);
+  parts = std::max<int64_t>(1, std::min<int64_t>(parts, passes));
   return launch_k(kern, dim3((unsigned)pages, (unsigned)parts), dim3(kThreads), smem, stream, true,
                   s, (const T*)K, k_stride, (const T*)V, v_stride, (uint8_t*)k_pages,
                   (uint8_t*)v_pages, k_scales, v_scales);

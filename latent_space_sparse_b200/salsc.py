@@ -485,6 +485,7 @@ class PagedCache:
         self.kv_shape = (self.n_tokens, n_kv_heads, head_dim)
         self.q_shape = (self.n_tokens, n_q_heads, head_dim)
         self.pool_shape = (n_pages, n_kv_heads, page_size, head_dim)
+        self.scale_shape = self.pool_shape[:2]
         self.desc = PageDesc(batch, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages,
                              self.n_tokens, max_q, page_table.data_ptr(), seq_lens.data_ptr(),
                              None if q_offsets is None else q_offsets.data_ptr(), float(rope_base),
@@ -509,18 +510,21 @@ class PagedCache:
         return stride[0] if shape[0] > 1 else 0
 
     def _pools(self, pools):
+        dev = self.device.index
         for i, t in enumerate(pools):
-            dt, shape = ((torch.float8_e4m3fn, self.pool_shape) if i < 2
-                         else (torch.float32, self.pool_shape[:2]))
-            if (t.dtype != dt or t.device != self.device or t.shape != shape
-                    or not t.is_contiguous()):
-                raise ValueError(f"pools must be contiguous {dt} {shape} on {self.device}")
+            if (t.dtype is not (torch.float8_e4m3fn if i < 2 else torch.float32)
+                    or t.shape != (self.pool_shape if i < 2 else self.scale_shape)
+                    or t.get_device() != dev or not t.is_contiguous()):
+                raise ValueError(f"pools must be contiguous float8_e4m3fn {self.pool_shape}, twice, "
+                                 f"then float32 {self.scale_shape}, twice, on {self.device}")
         return [t.data_ptr() for t in pools]
 
     def _call(self, fn, what, stream, *args):
-        if torch.cuda.current_device() == self.device.index:
-            s = stream if stream is not None else torch.cuda.current_stream()
-            st = fn(self._desc, *args, *self._ws, s.cuda_stream)
+        dev = self.device.index
+        if torch.cuda.current_device() == dev:
+            # the raw handle: a Stream object costs more than the launch
+            s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+            st = fn(self._desc, *args, *self._ws, s)
         else:
             with torch.cuda.device(self.device):
                 s = stream if stream is not None else torch.cuda.current_stream()
