@@ -139,13 +139,18 @@ struct PageWork {
   int tb;                  // new tokens of a row block
   int over;                // tiles' worth of time that a unit takes besides its tiles
   int rows;                // rows of a partial slot (>= tb * G)
+  int grid;                // CTAs
+  int overlaps;            // the kernel before on the stream need not have ended
   // Partial results of units that several CTAs share: CTA c's slots 2c (a
   // piece that starts inside a unit) and 2c + 1 (one that starts a unit and
   // does not end it), of `rows` rows each
   float* acc;     // [2 * grid][rows][d] unnormalised outputs
   float2* ml;     // [2 * grid][rows] running maximum (log2 units) and normaliser
+  // few rows: pieces of the unit that CTA c starts that are done (0 between calls)
+  uint32_t* done;  // [grid]
+  // many rows
   int4* info;     // [grid] of slot 2c + 1: first row's token row, KV head, rows, last CTA of the unit
-  void* qrot;     // many rows only: rotated queries and their rows' exponents (page_many.cu)
+  void* qrot;     // rotated queries and their rows' exponents (page_many.cu)
   int8_t* qexp;
 };
 
@@ -288,8 +293,57 @@ __device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem, int
   c.tile = rem > c.w.over ? (int)(rem - c.w.over) : 0;
 }
 
+// One row of a unit whose pieces are those of CTAs c0 .. c0 + n - 1:
+//   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i
+// CTA c0's second slot holds the unit's first piece, the following CTAs' first
+// slots the others.  A warp to a row, D / 32 dimensions a lane; the pieces'
+// maxima are read first, 32 at a time.  Reads past L1: other SMs wrote.
+template <typename T, int D>
+__device__ __forceinline__ void page_merge_row(const PageWork& w, int c0, int n, int r, T* dst) {
+  constexpr int kV = D / 32;
+  const int lane = threadIdx.x & 31;
+  auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * w.rows + r; };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(&w.ml[slot(i)]).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, acc[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float f = 0.f;
+    if (i0 + lane < n) {
+      const float2 ml = __ldcg(&w.ml[slot(i0 + lane)]);
+      // a piece without a token (m = -inf) weighs nothing; a NaN stays one
+      f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      l += f * ml.y;
+    }
+    const int top = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < top; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* a = w.acc + slot(i0 + i) * D + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 x = __ldcg((const float4*)a);
+        acc[0] = fmaf(fi, x.x, acc[0]);
+        acc[1] = fmaf(fi, x.y, acc[1]);
+        acc[2] = fmaf(fi, x.z, acc[2]);
+        acc[3] = fmaf(fi, x.w, acc[3]);
+      } else {
+        const float2 x = __ldcg((const float2*)a);
+        acc[0] = fmaf(fi, x.x, acc[0]);
+        acc[1] = fmaf(fi, x.y, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+  for (int k = 0; k < kV; ++k) dst[lane * kV + k] = from_f32<T>(l == 0.f ? 0.f : acc[k] / l);
+}
+
 // Host side: launchers.
-constexpr int kPageGrid = 148;  // CTAs of the attention kernels: one per SM
+constexpr int kPageGrid = 148;  // SMs
 cudaError_t launch_page_append(const PageStep& s, const void* K, int64_t k_stride, const void* V,
                                int64_t v_stride, void* k_pages, void* v_pages, float* k_scales,
                                float* v_scales, salsc_dtype dt, cudaStream_t stream);
@@ -298,8 +352,10 @@ cudaError_t launch_page_attend(const PageStep& s, const void* q, int64_t q_strid
                                const float* v_scales, void* out, void* part, salsc_dtype dt,
                                cudaStream_t stream);
 size_t page_attend_workspace(const PageStep& s, salsc_dtype dt);
+size_t page_attend_cleared();  // bytes at the workspace's start that are 0 between calls
 // The attention of few rows (page_few.cu): rows of its row blocks, and its launch.
-int page_few_rows(const PageStep& s, salsc_dtype dt);
+int page_few_rows(int64_t rows, salsc_dtype dt);  // for sequences of up to `rows` rows
+int page_few_grid(const PageStep& s, int rows, salsc_dtype dt);
 cudaError_t launch_page_few(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
                             const void* k_pages, const void* v_pages, const float* k_scales,
                             const float* v_scales, void* out, salsc_dtype dt, cudaStream_t stream);
@@ -308,7 +364,5 @@ constexpr int kPageManyRows = 256;
 cudaError_t launch_page_many(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
                              const void* k_pages, const void* v_pages, const float* k_scales,
                              const float* v_scales, void* out, cudaStream_t stream);
-cudaError_t launch_page_merge(const PageStep& s, const PageWork& w, void* out, salsc_dtype dt,
-                              cudaStream_t stream);
 
 }  // namespace salsc

@@ -91,7 +91,8 @@ salsc_status salsc_page_prepare(const salsc_page_desc* desc, void* ws, size_t ws
   salsc_status st = make_step(desc, &s);
   if (st != SALSC_OK) return st;
   if ((st = check_ws(desc, s, ws, ws_bytes)) != SALSC_OK) return st;
-  const cudaError_t e = cudaMemsetAsync(ws, 0, 16, (cudaStream_t)stream);
+  const cudaError_t e =
+      cudaMemsetAsync(ws, 0, kFlagsBytes + salsc::page_attend_cleared(), (cudaStream_t)stream);
   return e == cudaSuccess ? SALSC_OK : salsc::record_cuda_error(e);
 }
 

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 1024 : 768) / kThr
 page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, int64_t k_stride,
                    const T* __restrict__ V, int64_t v_stride, uint8_t* __restrict__ k_pages,
                    uint8_t* __restrict__ v_pages, float* __restrict__ k_scales,
-                   float* __restrict__ v_scales) {
+                   float* __restrict__ v_scales, int part) {
   extern __shared__ __align__(16) float cs[];  // [T][D/2] cos of the new tokens' slots, [T][D/2] sin
   __shared__ float red[2][kThreads / 32];
   constexpr int kHalf = D / 2;
@@ -184,14 +184,13 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
   // row of slot 0 (may lie before the first new row)
   const int64_t row0 = (int64_t)q.row0 + (q.m - m) + ((int64_t)j * s.T - start);
 
-  constexpr int kLogD = D == 128 ? 7 : 6;
+  constexpr int kLogD = D == 128 ? 7 : 6, kLogThreads = kThreads == 512 ? 9 : 8;
   const int log_per = s.log_t + kLogD - 5, per = 1 << log_per;  // threads of an item
-  const int items = kThreads >> log_per;                        // items of a pass
+  const int log_items = kLogThreads - log_per, items = 1 << log_items;  // items of a pass
   const int ti = tid & (per - 1), warps = per >> 5;
-  // this part's items, keys first, then values
-  const int passes = (2 * s.U + items - 1) / items;
-  const int first = (int)((int64_t)blockIdx.y * passes / gridDim.y);
-  const int last = (int)((int64_t)(blockIdx.y + 1) * passes / gridDim.y);
+  // this CTA's passes over the page's items, keys first, then values
+  const int passes = (2 * s.U + items - 1) >> log_items;
+  const int first = blockIdx.y * part, last = min(first + part, passes);
   for (int pass = first; pass < last; ++pass) {
     const int it = pass * items + (tid >> log_per);
     const bool live = it < 2 * s.U;
@@ -309,13 +308,14 @@ cudaError_t launch(const PageStep& s, const void* K, int64_t k_stride, const voi
     if (pages > s.n_tokens) pages = s.n_tokens;
   }
   const int per = s.T * D / 32, items = kThreads / per, passes = (2 * s.U + items - 1) / items;
-  // passes of a CTA: so many that it computes up to four cos and sin a thread for each
-  int64_t parts = passes / std::max(1, s.T * (D / 2) / kThreads / 4);
-  parts = std::max(parts, (kTargetCtas + pages - 1) / pages);
-  parts = std::max<int64_t>(1, std::min<int64_t>(parts, passes));
+  // Passes of a CTA: so many that it computes one cos and sin a thread for
+  // each; fewer where the step is small and CTAs would be missing.
+  int64_t part = std::max(1, s.T * (D / 2) / kThreads);
+  part = std::min(part, std::max<int64_t>(1, passes * pages / kTargetCtas));
+  const int64_t parts = (passes + part - 1) / part;
   return launch_k(kern, dim3((unsigned)pages, (unsigned)parts), dim3(kThreads), smem, stream, true,
                   s, (const T*)K, k_stride, (const T*)V, v_stride, (uint8_t*)k_pages,
-                  (uint8_t*)v_pages, k_scales, v_scales);
+                  (uint8_t*)v_pages, k_scales, v_scales, (int)part);
 }
 
 template <typename T>

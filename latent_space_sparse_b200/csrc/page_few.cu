@@ -23,7 +23,8 @@
 //
 // Work: tiles of 128 tokens of all units in one list, cut into equal ranges
 // for 148 persistent CTAs (page_sched.cuh); pieces of units that several CTAs
-// share leave (maximum, normaliser, sums) for the merge kernel.
+// share leave (maximum, normaliser, sums), and the CTA whose piece is done last
+// merges them.
 // Warps: 0-3 softmax (a thread per token; in the epilogue per output
 // dimension), 4 TMA producer (lanes issue a tile's pages), 5 MMA issuer.
 #include "page.cuh"
@@ -43,12 +44,17 @@ constexpr int kTerms = sizeof(T) == 4 ? 6 : 3;
 template <typename T, int D, int RC>
 struct Few {
   static constexpr int kN = (kTerms<T> * RC + 15) / 16 * 16;
-  static constexpr int kStages = D == 128 ? (kN > 48 ? 5 : 6) : 10;  // tiles in flight
-  static constexpr int kTileBytes = kPageTile * D;                   // of K, and of V
+  static constexpr int kTmem = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 3 * kN <= 256 ? 256 : 512;
+  // Two CTAs to an SM where tensor memory allows: one's tiles fly while the
+  // other is at a softmax or between units.
+  static constexpr int kCtas = kTmem <= 256 ? 2 : 1;
+  static constexpr int kTileBytes = kPageTile * D;  // of K, and of V
+  // tiles in flight: what fits with 4 KB for the static arrays
+  static constexpr int kStages = (226 * 1024 / kCtas - 5 * 1024 - 3 * kN * 128) / (2 * kTileBytes);
   static constexpr int kOffQ = kStages * 2 * kTileBytes;
   static constexpr int kOffP = kOffQ + kN * 128;
   static constexpr int kSmem = kOffP + 2 * kN * 128 + 1024;  // + alignment
-  static constexpr int kTmem = 3 * kN <= 64 ? 64 : 3 * kN <= 128 ? 128 : 3 * kN <= 256 ? 256 : 512;
+  static_assert(kStages >= 2, "tiles in flight");
 };
 
 // Scales and extent of one tile, written by the producer.
@@ -79,7 +85,7 @@ __device__ __forceinline__ bool has_nan(uint32_t w) {
 }
 
 template <typename T, int D, int RC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, Few<T, D, RC>::kCtas)
 page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
                 const T* __restrict__ q, int64_t q_stride, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const float* __restrict__ k_scales,
@@ -96,6 +102,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   __shared__ int rpos[RC];       // position of the row (a row that does not exist: -1)
   __shared__ int64_t rout[RC];   // its element offset in out
   __shared__ uint32_t tmem_base;
+  __shared__ bool joins;         // this CTA's piece is the last of its unit to be done
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t sm0 = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -121,12 +128,14 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   }
   if (warp == 5) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
   if (warp == 4 && lane < 2) tc::tma_prefetch_desc(lane ? &vmap : &kmap);
-  grid_dependency_wait();
+  // Behind page_many, which has waited for what came before it and runs on
+  // other sequences: this kernel's CTAs start where those have ended, and wait
+  // for all of them at their own end.
+  if (!w.overlaps) grid_dependency_wait();
   allow_dependent_launch();
   int64_t total, x0, x1, rem;
   int b;
   page_share(s, w, share, total, x0, x1, b, rem);
-  if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -517,9 +526,6 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           const float ll = wsum[0][tid] + wsum[1][tid] + wsum[2][tid] + wsum[3][tid];
           w.ml[(size_t)slot * w.rows + tid] = make_float2(mm, ll);
         }
-        if (tid == 0 && !whole && cur.tile == 0)
-          w.info[blockIdx.x] = make_int4(row0, cur.u, rows,
-                                         (int)share_of_tile(cur.last(), total, gridDim.x));
         if (warp * 32 < D) {
 #pragma unroll
           for (int r0 = 0; r0 < RC; r0 += 4) {
@@ -550,6 +556,21 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
             }
           }
         }
+        if (!whole) {
+          // the CTA whose piece is done last merges the unit's
+          const int c0 = (int)share_of_tile(cur.base + w.over, total, gridDim.x);
+          const int pieces = (int)share_of_tile(cur.last(), total, gridDim.x) - c0 + 1;
+          __threadfence();
+          tc::named_sync(1, kSoftmax);
+          if (tid == 0) {
+            joins = atomicAdd(&w.done[c0], 1u) == (uint32_t)pieces - 1;
+            if (joins) w.done[c0] = 0;
+            __threadfence();
+          }
+          tc::named_sync(1, kSoftmax);
+          if (joins)
+            for (int r = warp; r < rows; r += 4) page_merge_row<T, D>(w, c0, pieces, r, out + rout[r]);
+        }
         tc::fence_before_sync();
         tc::named_sync(1, kSoftmax);  // wsum, qfac, rpos, rout are free
         if (!cur.next_unit()) break;
@@ -558,6 +579,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   }
   __syncthreads();
   if (warp == 5) tc::tmem_dealloc(tmem, C::kTmem);
+  if (w.overlaps) grid_dependency_wait();
 }
 
 template <typename T, int D, int RC>
@@ -573,7 +595,7 @@ cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t 
   const uint64_t rows = (uint64_t)s.n_pages * s.U * s.T;
   if (!make_tmap_u8_rows(&km, kp, rows, D, s.T) || !make_tmap_u8_rows(&vm, vp, rows, D, s.T))
     return cudaErrorInvalidValue;
-  return launch_k(kern, dim3(kPageGrid), dim3(kThreads), C::kSmem, stream, true, s, w, (const T*)q,
+  return launch_k(kern, dim3(w.grid), dim3(kThreads), C::kSmem, stream, true, s, w, (const T*)q,
                   q_stride, km, vm, ks, vs, (T*)out);
 }
 
@@ -594,12 +616,16 @@ cudaError_t launch_d(int rc, const PageStep& s, const PageWork& w, const void* q
 
 }  // namespace
 
-int page_few_rows(const PageStep& s, salsc_dtype dt) {
+int page_few_rows(int64_t want, salsc_dtype dt) {
   const int most = dt == SALSC_F32 ? 16 : 32;
-  const int64_t want = (int64_t)s.max_q * s.G;
   int rc = 4;
   while (rc < most && rc < want) rc *= 2;
   return rc;
+}
+
+int page_few_grid(const PageStep&, int rows, salsc_dtype dt) {
+  const int n = (dt == SALSC_F32 ? kTerms<float> : kTerms<__nv_bfloat16>) * rows;
+  return n > 80 ? kPageGrid : 2 * kPageGrid;  // as Few::kCtas
 }
 
 cudaError_t launch_page_few(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
