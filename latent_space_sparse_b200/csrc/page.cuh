@@ -205,92 +205,75 @@ struct PageCursor {
   }
 };
 
-__device__ __forceinline__ int64_t page_seq_tiles(const PageStep& s, const PageWork& w, int b) {
-  const PageSeq q = page_seq(s, b);
-  const int64_t r = (int64_t)q.m * s.G;
-  if (r < w.min_rows || r > w.max_rows) return 0;
-  const PageBlocks p{q.n, q.m, w.tb, s.window, w.over};
-  return (int64_t)s.U * p.before(p.count());
-}
-
-// Block-wide: the length of the list of the kernel's sequences, this CTA's
-// range of it [x0, x1), and where x0 lies (b, and the place's index within
-// sequence b); b = -1 for an empty range.  sm: (blockDim / 32 + 2) int64.
-__device__ __forceinline__ void page_share(const PageStep& s, const PageWork& w, int64_t* sm,
-                                           int64_t& total, int64_t& x0, int64_t& x1, int& b,
-                                           int64_t& rem) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  total = 0;
-  // one pass for the total, a second one (from cached lengths) for the place;
-  // with one round of threads the first pass's counts are kept
-  int64_t mine = 0, end = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t run = 0;
-    if (pass == 1) {
-      x0 = share_begin(blockIdx.x, total, gridDim.x);
-      x1 = share_begin(blockIdx.x + 1, total, gridDim.x);
-      b = -1;
-      rem = 0;
-      if (x0 >= x1) return;
+// Warp-wide: the length of the list of the kernel's sequences, the end x1 of
+// this CTA's range of it, and the cursor at the range's start; false for an
+// empty range.  Every warp that needs it finds it for itself: no barrier.
+__device__ __forceinline__ bool page_begin(PageCursor& c, int64_t& total, int64_t& x1) {
+  const PageStep& s = c.s;
+  const PageWork& w = c.w;
+  const int lane = threadIdx.x & 31;
+  PageSeq q{};
+  int64_t cost = 0, end = 0;  // lane's sequence's places, and those up to it
+  auto scan = [&](int b0) {
+    cost = 0;
+    if (b0 + lane < s.B) {
+      q = page_seq(s, b0 + lane);
+      const int64_t r = (int64_t)q.m * s.G;
+      if (r >= w.min_rows && r <= w.max_rows) {
+        const PageBlocks p{q.n, q.m, w.tb, s.window, w.over};
+        cost = (int64_t)s.U * p.before(p.count());
+      }
     }
-    for (int b0 = 0; b0 < s.B; b0 += blockDim.x) {
-      if (pass == 0 || s.B > (int)blockDim.x) {
-        mine = b0 + tid < s.B ? page_seq_tiles(s, w, b0 + tid) : 0;
-        int64_t inc = mine;
+    end = cost;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t t = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += t;
-        }
-        __syncthreads();
-        if (lane == 31) sm[warp] = inc;
-        __syncthreads();
-        int64_t before = run;
-        for (int i = 0; i < warps; ++i) {
-          if (i < warp) before += sm[i];
-          run += sm[i];
-        }
-        end = before + inc;
-      }
-      if (pass == 1 && x0 >= end - mine && x0 < end) {
-        sm[warps] = b0 + tid;
-        sm[warps + 1] = x0 - (end - mine);
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += t;
     }
-    if (pass == 0) {
-      total = run;
-      __syncthreads();
-    }
+  };
+  total = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 32) {
+    scan(b0);
+    total += __shfl_sync(0xffffffffu, end, 31);
   }
-  __syncthreads();
-  b = (int)sm[warps];
-  rem = sm[warps + 1];
-}
-
-// Place a cursor on place `rem` of sequence b, which is place x0 of the list.
-// Every lane of the warp calls it, with the same arguments: the row block is
-// found by 32 tries at a time.
-__device__ __forceinline__ void page_seek(PageCursor& c, int b, int64_t rem, int64_t x0) {
-  c.b = b;
-  c.load();
-  // the row block: its U KV heads have U * tiles(k) tiles behind U * before(k)
-  const int64_t x = div_small(rem, c.s.U);
+  const int64_t each = div_small(total, gridDim.x), more = total - each * gridDim.x;
+  int64_t x = blockIdx.x * each + min((int64_t)blockIdx.x, more);  // share_begin
+  x1 = x + each + (blockIdx.x < more ? 1 : 0);
+  if (x >= x1) return false;
+  const int64_t x0 = x;
+  for (int b0 = 0;; b0 += 32) {
+    if (s.B > 32) scan(b0);  // one round of lanes is still at hand
+    const uint32_t hit = __ballot_sync(0xffffffffu, x < end);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      c.b = b0 + l;
+      c.blk = PageBlocks{__shfl_sync(0xffffffffu, q.n, l), __shfl_sync(0xffffffffu, q.m, l), w.tb, s.window,
+                         w.over};
+      c.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+      x -= __shfl_sync(0xffffffffu, end - cost, l);
+      break;
+    }
+    x -= __shfl_sync(0xffffffffu, end, 31);
+  }
+  // the row block: its U KV heads have U * cost behind U * before(k); 32 tries at a time
+  const int64_t y = div_small(x, s.U);
   int lo = 0, n = c.blk.count();  // the block is one of lo .. lo + n - 1
   while (n > 1) {
-    const int step = (n + 31) / 32, k = lo + (int)(threadIdx.x & 31) * step;
-    const bool at = k < lo + n && c.blk.before(k) <= x;
+    const int step = (n + 31) / 32, k = lo + lane * step;
+    const bool at = k < lo + n && c.blk.before(k) <= y;
     const int hit = __popc(__ballot_sync(0xffffffffu, at)) - 1;  // before() grows with k
     n = min(step, n - hit * step);
     lo += hit * step;
   }
   c.k = lo;
   c.tiles = c.blk.tiles(c.k);
-  rem -= (int64_t)c.s.U * c.blk.before(c.k);
-  const int cost = c.w.over + c.tiles;
-  c.u = (int)div_small(rem, cost);
-  rem -= (int64_t)c.u * cost;
-  c.base = x0 - rem;
-  c.tile = rem > c.w.over ? (int)(rem - c.w.over) : 0;
+  x -= (int64_t)s.U * c.blk.before(c.k);
+  const int unit = w.over + c.tiles;
+  c.u = (int)div_small(x, unit);
+  x -= (int64_t)c.u * unit;
+  c.base = x0 - x;
+  c.tile = x > w.over ? (int)(x - w.over) : 0;
+  return true;
 }
 
 // One row of a unit whose pieces are those of CTAs c0 .. c0 + n - 1:

@@ -79,6 +79,14 @@ __device__ __forceinline__ float2 f32x2(uint32_t c) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
 }
 
+// Atomic add that other threads' stores before the last barrier precede, and
+// that the block's loads after the next one follow, for the whole GPU.
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // A byte of w is the NaN code 0x7F or 0xFF.
 __device__ __forceinline__ bool has_nan(uint32_t w) {
   return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
@@ -95,7 +103,6 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   extern __shared__ unsigned char smem_raw[];
   __shared__ TileMeta meta[kStages];
   __shared__ alignas(8) uint64_t bars[3 * kStages + 7];
-  __shared__ int64_t share[kThreads / 32 + 2];
   __shared__ alignas(16) float wmax[2][4][RC];
   __shared__ alignas(16) float wsum[4][RC];
   __shared__ float qfac[RC];     // softmax scale * log2(e) / the row's power of two
@@ -133,9 +140,6 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   // for all of them at their own end.
   if (!w.overlaps) grid_dependency_wait();
   allow_dependent_launch();
-  int64_t total, x0, x1, rem;
-  int b;
-  page_share(s, w, share, total, x0, x1, b, rem);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -145,9 +149,9 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
     if (!dead && !tc::mbar_wait(bar, parity, s.flags)) dead = true;
   };
 
-  if (x0 < x1) {
-    PageCursor cur(s, w);
-    page_seek(cur, b, rem, x0);
+  PageCursor cur(s, w);
+  int64_t total, x1;
+  if (page_begin(cur, total, x1)) {
     int it = 0;  // tiles so far
     const int npg = kPageTile / s.T;
 
@@ -184,6 +188,13 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
             const bool mine = lane / npg == i - i0;
             const int sub = lane % npg;
             const uint32_t got = __ballot_sync(0xffffffffu, mine && pg >= 0);
+            // the copies first: the scales may still be on their way
+            if (mine && pg >= 0 && !dead) {
+              const uint32_t dst = sm0 + (uint32_t)st * 2 * kTile + (uint32_t)sub * s.T * D;
+              const int row = (pg * s.U + cur.u) * s.T;
+              tc::tma_load_2d(dst, &kmap, 0, row, kfull(st));
+              tc::tma_load_2d(dst + kTile, &vmap, 0, row, vfull(st));
+            }
             if (mine) {
               // value scale f * 2^e; zeros and what is not finite keep e = 0
               int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
@@ -196,18 +207,12 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               if (sub == 0) meta[st].loaded = got >> (npg * (i - i0));
             }
             __syncwarp();
-            const uint32_t bytes = dead ? 0u : (uint32_t)__popc(got) * s.T * D;
+            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine && pg >= 0 && !dead)) * s.T * D;
             if (lane == 0) {
               tc::mbar_expect_tx(kfull(st), bytes);
               tc::mbar_expect_tx(vfull(st), bytes);
             }
             __syncwarp();
-            if (mine && pg >= 0 && !dead) {
-              const uint32_t dst = sm0 + (uint32_t)st * 2 * kTile + (uint32_t)sub * s.T * D;
-              const int row = (pg * s.U + cur.u) * s.T;
-              tc::tma_load_2d(dst, &kmap, 0, row, kfull(st));
-              tc::tma_load_2d(dst + kTile, &vmap, 0, row, vfull(st));
-            }
           }
           pg = pg_n;
           ks = ks_n;
@@ -560,12 +565,10 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           // the CTA whose piece is done last merges the unit's
           const int c0 = (int)share_of_tile(cur.base + w.over, total, gridDim.x);
           const int pieces = (int)share_of_tile(cur.last(), total, gridDim.x) - c0 + 1;
-          __threadfence();
           tc::named_sync(1, kSoftmax);
           if (tid == 0) {
-            joins = atomicAdd(&w.done[c0], 1u) == (uint32_t)pieces - 1;
+            joins = add_acq_rel(&w.done[c0], 1u) == (uint32_t)pieces - 1;
             if (joins) w.done[c0] = 0;
-            __threadfence();
           }
           tc::named_sync(1, kSoftmax);
           if (joins)

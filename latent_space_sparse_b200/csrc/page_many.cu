@@ -67,7 +67,6 @@ struct Shared {
   TileScales meta[kRing];
   uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
   uint64_t bars[22 + kSegments];
-  int64_t share[kThreads / 32 + 2];
   uint32_t tmem_base;
 };
 
@@ -257,9 +256,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   if (tid < 2 * kRing * 4) sh.nan[tid / 4][tid % 4] = 0;
   grid_dependency_wait();
   allow_dependent_launch();
-  int64_t total, x0, x1, rem;
-  int b;
-  page_share(s, w, sh.share, total, x0, x1, b, rem);
   if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc::fence_before_sync();
   __syncthreads();
@@ -271,7 +267,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   };
   const int tb2 = w.tb / 2;  // new tokens of a half
 
-  if (x0 < x1) {
+  {
     int it = 0;  // tiles so far
     auto segment = [&](int i) -> const Segment& {
       wait(segfull(i), (i / kSegments) & 1);
@@ -345,9 +341,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       // ------------------------------------------------ pages to shared memory
       if (warp == 13) {
         PageCursor cur(s, w);
-        page_seek(cur, b, rem, x0);
+        int64_t total, x1;
+        const bool any = page_begin(cur, total, x1);
         for (int seg = 0;; ++seg) {
-          const int n = cur.upto(x1);
+          const int n = any ? cur.upto(x1) : 0;
           if (n <= 0) {
             if (lane == 0) {
               sh.segments[seg % kSegments].n = 0;
