@@ -5,23 +5,78 @@
 namespace salsc {
 namespace {
 
-constexpr int kMergeWarps = 4;  // rows of a merge CTA
+constexpr int kMergeWarps = 4, kMergeRows = 4;  // warps of a merge CTA, rows of a warp
 // What a unit takes besides its tiles, in tiles.
-constexpr int kOverFew = 2, kOverMany = 3;
+constexpr int kOverFew = 3, kOverMany = 3;
 
+// A warp takes kMergeRows rows of the unit that CTA c starts (usually of two
+// pieces): lane (row, piece) reads a piece's maximum and normaliser, and the
+// pieces' outputs of all rows are loaded together.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 page_merge_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
                   __nv_bfloat16* __restrict__ out) {
-  const int c = blockIdx.x;
-  const int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  constexpr int kV = D / 32, kPieces = 32 / kMergeRows;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kMergeRows;
   grid_dependency_wait();
   allow_dependent_launch();
   const int4 info = w.info[c];
-  if (r >= info.z) return;
-  const int i = r / s.G, g = r - i * s.G;
-  page_merge_row<__nv_bfloat16, D>(w, c, info.w - c + 1, r,
-                                   out + ((int64_t)(info.x + i) * s.Hq + info.y * s.G + g) * D);
+  if (r0 >= info.z) return;
+  const int n = info.w - c + 1;  // pieces
+  auto slot = [&](int i, int r) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * w.rows + r; };
+  const int mr = lane / kPieces, mp = lane % kPieces, rr = min(r0 + mr, info.z - 1);
+  float m = -INFINITY;
+  for (int i = mp; i < n; i += kPieces) m = fmaxf(m, w.ml[slot(i, rr)].x);
+#pragma unroll
+  for (int o = kPieces / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, acc[kMergeRows][kV];
+#pragma unroll
+  for (int r = 0; r < kMergeRows; ++r)
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[r][k] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kPieces) {
+    float f = 0.f;
+    if (i0 + mp < n) {
+      const float2 ml = w.ml[slot(i0 + mp, rr)];
+      // a piece without a token (m = -inf) weighs nothing; a NaN stays one
+      f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      l += f * ml.y;
+    }
+    const int top = min(kPieces, n - i0);
+#pragma unroll 2
+    for (int i = 0; i < top; ++i) {
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        const float fi = __shfl_sync(0xffffffffu, f, r * kPieces + i);
+        const float* a = w.acc + slot(i0 + i, min(r0 + r, info.z - 1)) * D + lane * kV;
+        if constexpr (kV == 4) {
+          const float4 x = *(const float4*)a;
+          acc[r][0] = fmaf(fi, x.x, acc[r][0]);
+          acc[r][1] = fmaf(fi, x.y, acc[r][1]);
+          acc[r][2] = fmaf(fi, x.z, acc[r][2]);
+          acc[r][3] = fmaf(fi, x.w, acc[r][3]);
+        } else {
+          const float2 x = *(const float2*)a;
+          acc[r][0] = fmaf(fi, x.x, acc[r][0]);
+          acc[r][1] = fmaf(fi, x.y, acc[r][1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = kPieces / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+  for (int r = 0; r < kMergeRows; ++r) {
+    const float lr = __shfl_sync(0xffffffffu, l, r * kPieces);
+    if (r0 + r >= info.z) break;
+    const int i = (r0 + r) / s.G, g = r0 + r - i * s.G;
+    __nv_bfloat16* dst = out + ((int64_t)(info.x + i) * s.Hq + info.y * s.G + g) * D + lane * kV;
+#pragma unroll
+    for (int k = 0; k < kV; k += 2)
+      *(__nv_bfloat162*)(dst + k) = __floats2bfloat162_rn(lr == 0.f ? 0.f : acc[r][k] / lr,
+                                                          lr == 0.f ? 0.f : acc[r][k + 1] / lr);
+  }
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -83,7 +138,7 @@ Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
 }
 
 cudaError_t launch_merge(const PageStep& s, const PageWork& w, void* out, cudaStream_t stream) {
-  const dim3 grid(w.grid, (unsigned)((w.rows + kMergeWarps - 1) / kMergeWarps));
+  const dim3 grid(w.grid, (unsigned)(w.rows / (kMergeWarps * kMergeRows)));
   return launch_k(s.d == 64 ? page_merge_kernel<64> : page_merge_kernel<128>, grid, dim3(kMergeWarps * 32),
                   0, stream, true, s, w, (__nv_bfloat16*)out);
 }

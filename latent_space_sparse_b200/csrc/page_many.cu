@@ -127,16 +127,19 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 
 // Queries of the sequences that this file's attention takes, rotated, as f16
 // times a power of two for each row: qrot [n_tokens][Hq][d], exponents
-// qexp [n_tokens][Hq].  A warp per token: lanes hold two (d = 64: one) pairs,
-// whose cos and sin serve all heads.  Bound by memory: 2 bytes in, 2 out.
-constexpr int kRotateWarps = 8;
+// qexp [n_tokens][Hq].  A warp per token and kRotateHeads heads, whose rows it
+// loads at once; lanes hold two (d = 64: one) pairs, whose cos and sin serve
+// those heads.  Bound by memory: 2 bytes in, 2 out.  (A warp per token with
+// all its heads waited for four rows at a time: 18 against XXX us for 4096
+// tokens of 32 heads.)
+constexpr int kRotateWarps = 8, kRotateHeads = 8;
 template <int D>
 __global__ void __launch_bounds__(kRotateWarps * 32)
 page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,
                    const __nv_bfloat16* __restrict__ q, int64_t q_stride) {
   constexpr int kP = D / 64;  // pairs of a lane
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRotateWarps + (threadIdx.x >> 5);
+  const int t = blockIdx.x * kRotateWarps + (threadIdx.x >> 5), h0 = blockIdx.y * kRotateHeads;
   grid_dependency_wait();
   allow_dependent_launch();
   if (t >= s.n_tokens) return;
@@ -153,55 +156,51 @@ page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ P
   const int64_t rows = (int64_t)sq.m * s.G;
   if (rows < w.min_rows || rows > w.max_rows || t < sq.row0 || t >= sq.row0 + sq.m) return;
   const int pos = sq.n - sq.m + (t - sq.row0);
+  const __nv_bfloat16* src = q + (int64_t)t * q_stride + kP * lane;
+  uint32_t xa[kRotateHeads], xb[kRotateHeads];  // d = 64: one element each
+#pragma unroll
+  for (int j = 0; j < kRotateHeads; ++j) {
+    const int h = min(h0 + j, s.Hq - 1);
+    if constexpr (kP == 2) {
+      xa[j] = *(const uint32_t*)(src + h * D);
+      xb[j] = *(const uint32_t*)(src + h * D + D / 2);
+    } else {
+      xa[j] = *(const uint16_t*)(src + h * D);
+      xb[j] = *(const uint16_t*)(src + h * D + D / 2);
+    }
+  }
   float c[kP], sn[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) {
     c[i] = 1.f, sn[i] = 0.f;
     if (s.rotate && pos >= 0) page_cs(pos, s.turns[kP * lane + i], c[i], sn[i]);
   }
-  const __nv_bfloat16* src = q + (int64_t)t * q_stride + kP * lane;
   __half* dst = (__half*)w.qrot + (int64_t)t * s.Hq * D + kP * lane;
-  constexpr int kBatch = 4;  // rows in flight
-  for (int h0 = 0; h0 < s.Hq; h0 += kBatch) {
-    float x[kBatch][kP], y[kBatch][kP];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int h = min(h0 + j, s.Hq - 1);
-      if constexpr (kP == 2) {
-        const uint32_t a = *(const uint32_t*)(src + h * D), b2 = *(const uint32_t*)(src + h * D + D / 2);
-        x[j][0] = __uint_as_float(a << 16), x[j][1] = __uint_as_float(a & 0xFFFF0000u);
-        y[j][0] = __uint_as_float(b2 << 16), y[j][1] = __uint_as_float(b2 & 0xFFFF0000u);
-      } else {
-        x[j][0] = __bfloat162float(src[h * D]);
-        y[j][0] = __bfloat162float(src[h * D + D / 2]);
-      }
+  for (int j = 0; j < kRotateHeads; ++j) {
+    const int h = h0 + j;
+    float x[kP], y[kP], am = 0.f;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const float a = __uint_as_float(i ? xa[j] & 0xFFFF0000u : xa[j] << 16);
+      const float b2 = __uint_as_float(i ? xb[j] & 0xFFFF0000u : xb[j] << 16);
+      x[i] = a * c[i] - b2 * sn[i], y[i] = b2 * c[i] + a * sn[i];
+      am = fmaxf(am, fmaxf(fabsf(x[i]), fabsf(y[i])));
     }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int h = h0 + j;
-      float am = 0.f;
-#pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        const float a = x[j][i] * c[i] - y[j][i] * sn[i], b2 = y[j][i] * c[i] + x[j][i] * sn[i];
-        x[j][i] = a, y[j][i] = b2;
-        am = fmaxf(am, fmaxf(fabsf(a), fabsf(b2)));
+    asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(am));
+    // power of two that brings the row's largest element into [2^7, 2^8)
+    int ex = (int)(__float_as_uint(am) >> 23) - 127 - 7;
+    ex = min(max(ex, -119), 119);
+    const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
+    if (h < s.Hq) {
+      if constexpr (kP == 2) {
+        *(uint32_t*)(dst + h * D) = half2_bits(x[0] * mul, x[1] * mul);
+        *(uint32_t*)(dst + h * D + D / 2) = half2_bits(y[0] * mul, y[1] * mul);
+      } else {
+        dst[h * D] = __float2half_rn(x[0] * mul);
+        dst[h * D + D / 2] = __float2half_rn(y[0] * mul);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-      // power of two that brings the row's largest element into [2^7, 2^8)
-      int ex = (int)(__float_as_uint(am) >> 23) - 127 - 7;
-      ex = min(max(ex, -119), 119);
-      const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
-      if (h < s.Hq) {
-        if constexpr (kP == 2) {
-          *(uint32_t*)(dst + h * D) = half2_bits(x[j][0] * mul, x[j][1] * mul);
-          *(uint32_t*)(dst + h * D + D / 2) = half2_bits(y[j][0] * mul, y[j][1] * mul);
-        } else {
-          dst[h * D] = __float2half_rn(x[j][0] * mul);
-          dst[h * D + D / 2] = __float2half_rn(y[j][0] * mul);
-        }
-        if (lane == 0) w.qexp[(int64_t)t * s.Hq + h] = (int8_t)ex;
-      }
+      if (lane == 0) w.qexp[(int64_t)t * s.Hq + h] = (int8_t)ex;
     }
   }
 }
@@ -749,7 +748,8 @@ cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t 
   if (!make_tmap_f16_heads(&qm, w.qrot, s.n_tokens, s.Hq, D, w.tb / 2, s.G) ||
       !make_tmap_u8_rows(&km, kp, rows, D, s.T) || !make_tmap_u8_rows(&vm, vp, rows, D, s.T))
     return cudaErrorInvalidValue;
-  e = launch_k(page_rotate_kernel<D>, dim3((unsigned)((s.n_tokens + kRotateWarps - 1) / kRotateWarps)),
+  e = launch_k(page_rotate_kernel<D>, dim3((unsigned)((s.n_tokens + kRotateWarps - 1) / kRotateWarps),
+                    (unsigned)((s.Hq + kRotateHeads - 1) / kRotateHeads)),
                dim3(kRotateWarps * 32), 0, stream, true, s, w, (const __nv_bfloat16*)q, q_stride);
   if (e != cudaSuccess) return e;
   return launch_k(kern, dim3(kPageGrid), dim3(kThreads), Many<D>::kSmem, stream, true, s, w, qm, km, vm,
