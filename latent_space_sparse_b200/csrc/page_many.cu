@@ -16,9 +16,11 @@
 // the normaliser as p * 2^-e; f and both scales' signs go into the f16 values.
 // So the weights 2^(t - m) stay in f16's range whatever the scales are.
 //
-// The maximum that the weights refer to follows the rows' maximum only when
-// that has grown by more than kSlack: weights up to 2^kSlack hold as well in
-// f16, and O is rescaled a few times in a row's life and not once per tile.
+// The weights refer to a maximum that follows the rows' only when it must: a
+// tile's weights are computed with what is at hand, and only if their sum
+// reaches kMost (none is larger then, and f16 holds them as well) computed again
+// with the tile's own maximum, when O is rescaled too.  So no maximum stands
+// between the scores and the exponentials of most tiles.
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of a half (a
 // thread per row), warps 8-11 cache tiles (codes to f16), warp 12 issues the
@@ -36,9 +38,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kConvert = 128;   // threads of the converting warps
-constexpr int kEarly = 96;     // of a tile's 128 weights: handed on while the others are computed
 constexpr int kRing = 4;        // tiles whose scales are kept
-constexpr float kSlack = 8.f;   // log2 units
+constexpr float kMost = 256.f;  // sum of a tile's weights that the maximum must follow
 
 // What the copying warp says of a tile, by group of 16 tokens.
 struct alignas(16) TileScales {  // read by float4
@@ -66,7 +67,7 @@ struct Shared {
   Segment segments[kSegments];
   TileScales meta[kRing];
   uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
-  uint64_t bars[22 + kSegments];
+  uint64_t bars[20 + kSegments];
   uint32_t tmem_base;
 };
 
@@ -226,7 +227,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   auto sready = [&](int h) { return bar0 + 8u * (8 + h); };
   auto pready = [&](int h) { return bar0 + 8u * (10 + h); };
   auto odone = [&](int h) { return bar0 + 8u * (12 + h); };
-  auto pearly = [&](int h) { return bar0 + 8u * (20 + kSegments + h); };  // the first kEarly weights
+
   const uint32_t qfull = bar0 + 8u * 14, qfree = bar0 + 8u * 15;
   auto cfull = [&](int v) { return bar0 + 8u * (16 + v); };  // codes of K, of V
   auto cfree = [&](int v) { return bar0 + 8u * (18 + v); };
@@ -241,7 +242,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       tc::mbar_init(sready(i), 2);  // the scores, and the issuer for what it has waited for
       tc::mbar_init(pready(i), 128);
       tc::mbar_init(odone(i), 1);
-      tc::mbar_init(pearly(i), 128);
       tc::mbar_init(cfull(i), 1);
       tc::mbar_init(cfree(i), kConvert);
     }
@@ -297,17 +297,12 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         auto values = [&](int h, int i, bool first) {
           const uint64_t va =
               tc::sdesc_mnmajor_sw128(sm0 + C::kOffV + (uint32_t)(i & 1) * C::kTileBytes, 16384, 1024);
-          wait(pearly(h), cnt[h] & 1);
+          wait(pready(h), cnt[h]++ & 1);
           tc::fence_after_sync();
 #pragma unroll
-          for (int kk = 0; kk < kPageTile / 16; ++kk) {
-            if (kk == kEarly / 16) {
-              wait(pready(h), cnt[h]++ & 1);
-              tc::fence_after_sync();
-            }
+          for (int kk = 0; kk < kPageTile / 16; ++kk)
             tc::mma_ts_lead(lead, tmem + C::kColO + h * D, tmem + h * 128 + kk * 8, va + (kk * 2048 >> 4), id_o,
-                           !first || kk > 0);
-          }
+                            !first || kk > 0);
           tc::commit_lead(lead, odone(h));
         };
         for (int seg = 0;; ++seg) {
@@ -628,24 +623,53 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
 #pragma unroll
             for (int c0 = 0; c0 < kPageTile; c0 += 32) tc::tmem_ld32(cs + c0, t + c0);
             tc::tmem_ld_wait();
-            // eight chains side by side: one alone would wait for each of its steps
-            float a[8];
+            const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] = fmaxf(t[16 * k], t[16 * k + 1]);
+            for (int k = 0; k < 8; ++k) {
+              const float c = masked ? 1.f : mt.ks[k] * fac, d = (masked ? 0.f : mt.ve[k]) - ref;
 #pragma unroll
-            for (int j = 2; j < 16; j += 2)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) a[k] = max3(a[k], t[16 * k + j], t[16 * k + j + 1]);
-            if (!masked) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) a[k] = fmaf(a[k], mt.ks[k] * fac, mt.ve[k]);
+              for (int j = 16 * k; j < 16 * k + 16; j += 2) fma2(t[j], t[j + 1], c, d);
             }
-            const float mt_ = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
-            const bool grow = mt_ > m + kSlack || (m == -INFINITY && mt_ > m);
-            if (__any_sync(0xffffffffu, grow)) {
-              const float al = grow ? ex2(m - mt_) : 1.f;  // 0 from m = -inf
-              if (grow) m = mt_;
+            float lt;
+            bool known = i > 0;  // m is worth a try
+            for (bool last = false;; last = true) {
+              if (known) {
+                float total = 0.f;
+                lt = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  float sum0 = 0.f, sum1 = 0.f;
+                  uint32_t pk[8];
+#pragma unroll
+                  for (int j = 0; j < 16; j += 2) {
+                    const float a0 = ex2(t[16 * k + j]), a1 = ex2(t[16 * k + j + 1]);
+                    add2(sum0, sum1, a0, a1);
+                    pk[j / 2] = half2_bits(a0, a1);
+                  }
+                  sum0 += sum1;
+                  total += sum0;
+                  lt = fmaf(sum0, mt.ive[k], lt);
+                  tc::tmem_st8(cs + 8 * k, pk);  // the weights take the scores' place
+                }
+                if (last || !__any_sync(0xffffffffu, !(total < kMost) || m == -INFINITY)) break;
+              }
+              // go by this tile's maximum
+              known = true;
+              float a[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) a[k] = fmaxf(t[16 * k], t[16 * k + 1]);
+#pragma unroll
+              for (int j = 2; j < 16; j += 2)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a[k] = max3(a[k], t[16 * k + j], t[16 * k + j + 1]);
+              const float top = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+              const bool none = m == -INFINITY;
+              const float by = top > 0.f || (none && top > -INFINITY) ? top : 0.f;
+              const float al = none ? 0.f : ex2(-by);
+              if (!none || top > -INFINITY) m = (none ? 0.f : m) + by;
               l *= al;
+#pragma unroll
+              for (int j = 0; j < kPageTile; ++j) t[j] -= by;
               if (i > 0) {  // the sums so far (of this piece) follow
                 wait(odone(h), (cnt - 1) & 1);
                 tc::fence_after_sync();
@@ -660,29 +684,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
                 }
               }
             }
-            const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float c = masked ? 1.f : mt.ks[k] * fac, d = (masked ? 0.f : mt.ve[k]) - ref;
-              float sum0 = 0.f, sum1 = 0.f;
-              uint32_t pk[8];
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float a0 = t[16 * k + j], a1 = t[16 * k + j + 1];
-                fma2(a0, a1, c, d);
-                a0 = ex2(a0);
-                a1 = ex2(a1);
-                add2(sum0, sum1, a0, a1);
-                pk[j / 2] = half2_bits(a0, a1);
-              }
-              l = fmaf(sum0 + sum1, mt.ive[k], l);
-              tc::tmem_st8(cs + 8 * k, pk);  // the weights take the scores' place
-              if (k == kEarly / 16 - 1) {
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                tc::mbar_arrive(pearly(h));
-              }
-            }
+            l += lt;
             tc::tmem_st_wait();
             tc::fence_before_sync();
             tc::mbar_arrive(pready(h));
