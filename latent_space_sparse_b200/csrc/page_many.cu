@@ -262,7 +262,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   const uint32_t tmem = sh.tmem_base;
   bool dead = false;  // a wait gave up: skip the others, so that the kernel ends
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!dead && !tc::mbar_wait_long(bar, parity, s.flags)) dead = true;
+    if (!dead && !tc::mbar_wait(bar, parity, s.flags)) dead = true;
   };
   const int tb2 = w.tb / 2;  // new tokens of a half
 
@@ -272,9 +272,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       wait(segfull(i), (i / kSegments) & 1);
       return sh.segments[i % kSegments];
     };
-    // 192 * 256 + 72 * 128 + 56 * 128 = 128 * 512 registers
+    // 200 * 256 + 64 * 128 + 48 * 128 = 128 * 512 registers
     if (warp >= 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
       // ------------------------------------------------ MMA issuer
       // All lanes run it, so that the compiler sees that descriptors and addresses
       // are the warp's and keeps them in uniform registers; one lane issues.
@@ -441,7 +441,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       }
       __syncwarp();
     } else if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
       // ------------------------------------------------ cache tiles
       // A pass is 32 rows by 64 codes: a warp's lanes hold 16 codes each of 8
       // rows, and eight lanes that access shared memory together those of rows
@@ -555,7 +555,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         }
       }
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
       // ------------------------------------------------ softmax
       const int h = warp >> 2, r = tid & 127;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);

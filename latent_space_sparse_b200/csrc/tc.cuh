@@ -88,36 +88,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
   return mbar_wait_limit(bar, parity, flags, kWaitLimitNs);
 }
 
-// mbar_wait as a short loop that looks at the clock once in 4096 tries (each of which the
-// hardware suspends for a while): waiting warps take few issue slots from those that work.
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint32_t* flags) {
-  uint64_t t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, 0;\n"
-        "LAB_TRY:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra LAB_END;\n\t"
-        "add.u32 n, n, 1;\n\t"
-        "setp.lt.u32 q, n, 4096;\n\t"
-        "@q bra LAB_TRY;\n"
-        "LAB_END:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
-      if (flags) atomicOr(flags, FLAG_WAIT_TIMEOUT);
-      return false;
-    }
-  }
-}
-
 // ---------------------------------------------------------------- TMA
 
 // 2-D tiled load of one box into shared memory, completing on `bar`.
@@ -205,18 +175,9 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
-// The same with A in tensor memory (a row to a lane, two 16-bit elements to a column).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The two above and mma_commit for code that a whole warp runs: the lane with `lead` issues.
+// mma_bf16 (for f16 inputs too: the instruction descriptor says which), the same with A in tensor
+// memory (a row to a lane, two elements to a column), and mma_commit, for code that a whole warp
+// runs: the lane with `lead` issues.
 __device__ __forceinline__ void mma_lead(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
