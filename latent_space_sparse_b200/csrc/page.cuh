@@ -97,30 +97,44 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float m) {
       : "f"(m));
 }
 
-// Item x of a list in which sequence b has count(b) items: the sequence (-1 when
-// x is past the end) and the item's index in it.  Every warp finds it for
-// itself, without a barrier; all lanes call it, with the same x.
-template <typename F>
-__device__ __forceinline__ void page_find(int B, int x, F count, int& b_out, int& r_out) {
+// Item x of a list in which sequence b has cost(b) items: the sequence (false
+// when x is past the end), and x becomes the item's index in it.  A warp finds
+// it for itself, without a barrier: each lane adds up a 32nd of the sequences,
+// then of those of the lane that holds x, and so on.  After the last round lane
+// i has called cost(b0 + i) last, and the sequence is that of lane b - b0.
+// start(total) says what x is once the length of the list is known.
+template <typename F, typename S>
+__device__ __forceinline__ bool page_find(int B, F cost, S start, int64_t& x, int& b, int& b0) {
   const int lane = threadIdx.x & 31;
-  b_out = -1;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int c = b0 + lane < B ? count(b0 + lane) : 0;
-    int end = c;
+  int lo = 0, n = B;
+  for (bool first = true;; first = false) {
+    const int c = (n + 31) / 32;
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < c; ++i) {
+      const int k = lane * c + i;
+      if (k < n) sum += cost(lo + k);
+    }
+    int64_t end = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, end, o);
+      const int64_t t = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += t;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, x < end);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      b_out = b0 + l;
-      r_out = x - __shfl_sync(0xffffffffu, end - c, l);
-      return;
+    if (first) {
+      const int64_t total = __shfl_sync(0xffffffffu, end, 31);
+      x = start(total);
+      if (x >= total) return false;
     }
-    x -= __shfl_sync(0xffffffffu, end, 31);
+    const int l = __ffs(__ballot_sync(0xffffffffu, x < end)) - 1;
+    x -= __shfl_sync(0xffffffffu, end - sum, l);
+    b0 = lo;
+    lo += l * c;
+    n = min(c, n - l * c);
+    if (c == 1) break;
   }
+  b = lo;
+  return true;
 }
 
 // cos and sin of position pos at `turns` (of 2^64) turns per position: the
@@ -212,49 +226,30 @@ __device__ __forceinline__ bool page_begin(PageCursor& c, int64_t& total, int64_
   const PageStep& s = c.s;
   const PageWork& w = c.w;
   const int lane = threadIdx.x & 31;
-  PageSeq q{};
-  int64_t cost = 0, end = 0;  // lane's sequence's places, and those up to it
-  auto scan = [&](int b0) {
-    cost = 0;
-    if (b0 + lane < s.B) {
-      q = page_seq(s, b0 + lane);
-      const int64_t r = (int64_t)q.m * s.G;
-      if (r >= w.min_rows && r <= w.max_rows) {
+  PageSeq q{};  // of the sequence that the lane looked at last
+  int64_t x, x0;
+  int b0;
+  const bool any = page_find(
+      s.B,
+      [&](int b) -> int64_t {
+        q = page_seq(s, b);
+        const int64_t r = (int64_t)q.m * s.G;
+        if (r < w.min_rows || r > w.max_rows) return 0;
         const PageBlocks p{q.n, q.m, w.tb, s.window, w.over};
-        cost = (int64_t)s.U * p.before(p.count());
-      }
-    }
-    end = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += t;
-    }
-  };
-  total = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 32) {
-    scan(b0);
-    total += __shfl_sync(0xffffffffu, end, 31);
-  }
-  const int64_t each = div_small(total, gridDim.x), more = total - each * gridDim.x;
-  int64_t x = blockIdx.x * each + min((int64_t)blockIdx.x, more);  // share_begin
-  x1 = x + each + (blockIdx.x < more ? 1 : 0);
-  if (x >= x1) return false;
-  const int64_t x0 = x;
-  for (int b0 = 0;; b0 += 32) {
-    if (s.B > 32) scan(b0);  // one round of lanes is still at hand
-    const uint32_t hit = __ballot_sync(0xffffffffu, x < end);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      c.b = b0 + l;
-      c.blk = PageBlocks{__shfl_sync(0xffffffffu, q.n, l), __shfl_sync(0xffffffffu, q.m, l), w.tb, s.window,
-                         w.over};
-      c.row0 = __shfl_sync(0xffffffffu, q.row0, l);
-      x -= __shfl_sync(0xffffffffu, end - cost, l);
-      break;
-    }
-    x -= __shfl_sync(0xffffffffu, end, 31);
-  }
+        return (int64_t)s.U * p.before(p.count());
+      },
+      [&](int64_t all) {
+        total = all;
+        const int64_t each = div_small(all, gridDim.x), more = all - each * gridDim.x;
+        x0 = blockIdx.x * each + min((int64_t)blockIdx.x, more);  // share_begin
+        x1 = x0 + each + (blockIdx.x < more ? 1 : 0);
+        return x0 < x1 ? x0 : all;
+      },
+      x, c.b, b0);
+  if (!any) return false;
+  const int l = c.b - b0;
+  c.blk = PageBlocks{__shfl_sync(0xffffffffu, q.n, l), __shfl_sync(0xffffffffu, q.m, l), w.tb, s.window, w.over};
+  c.row0 = __shfl_sync(0xffffffffu, q.row0, l);
   // the row block: its U KV heads have U * cost behind U * before(k); 32 tries at a time
   const int64_t y = div_small(x, s.U);
   int lo = 0, n = c.blk.count();  // the block is one of lo .. lo + n - 1

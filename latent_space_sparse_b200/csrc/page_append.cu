@@ -167,16 +167,25 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
   grid_dependency_wait();
   allow_dependent_launch();
 
-  // the x-th touched page of the step
-  int b, j = 0;
-  page_find(s.B, blockIdx.x, [&](int i) {
-    const PageSeq q = page_seq(s, i);
-    const int m = min(q.m, q.n);
-    return m > 0 ? ((q.n - 1) >> s.log_t) - ((q.n - m) >> s.log_t) + 1 : 0;
-  }, b, j);
-  if (b < 0) return;
+  // the x-th touched page of the step; without offsets a sequence touches one
+  int b = blockIdx.x, j = 0;
+  if (s.offs) {
+    int64_t x;
+    int b0;
+    const bool any = page_find(
+        s.B,
+        [&](int i) -> int64_t {
+          const PageSeq q = page_seq(s, i);
+          const int m = min(q.m, q.n);
+          return m > 0 ? ((q.n - 1) >> s.log_t) - ((q.n - m) >> s.log_t) + 1 : 0;
+        },
+        [&](int64_t) { return (int64_t)blockIdx.x; }, x, b, b0);
+    if (!any) return;
+    j = (int)x;
+  }
   const PageSeq q = page_seq(s, b);
   const int m = min(q.m, q.n), start = q.n - m;
+  if (m <= 0) return;
   j += start >> s.log_t;
   const int pg = page_of(s, b, j);
   if (pg < 0) return;

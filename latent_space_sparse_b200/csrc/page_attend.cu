@@ -88,8 +88,6 @@ PageWork layout(const PageStep& s, int rows, int grid, void* part, size_t& off) 
   w.rows = rows;
   w.grid = grid;
   char* p = (char*)part;
-  w.done = (uint32_t*)(p + off);
-  off = align_up(off + sizeof(uint32_t) * grid);
   w.info = (int4*)(p + off);
   off = align_up(off + sizeof(int4) * grid);
   w.ml = (float2*)(p + off);
@@ -99,11 +97,14 @@ PageWork layout(const PageStep& s, int rows, int grid, void* part, size_t& off) 
   return w;
 }
 
-// The kernels of a step.  fp32 storage, and steps of few new tokens a sequence:
-// page_few alone.  Otherwise page_few takes the sequences with a single new
-// token (its cost grows with the rows that it is built for: one for 32 rows
-// took XX us longer on a step of prompts and single tokens) and page_many the
-// others.
+// The kernels of a step.  page_few takes sequences of up to 16 rows (new tokens
+// times heads per KV head) and all of fp32 storage, page_many the others: at 16
+// rows page_few takes 37 us and page_many 48 (16 sequences of 8192 tokens, 16
+// heads on one KV head), at 20 rows page_many 72 us and a page_few for 32 rows
+// 95 (4 sequences of 8192, 5 new tokens, 32 heads on 8).  A step that has both
+// kinds sends page_few the sequences with a single new token only: its time
+// grows with the rows that it is built for (eight requests of 1 to 1024 new
+// tokens: 237 us with one for 32 rows, 208 with one for 4).
 struct Plan {
   PageWork few, many;
   bool has_many;
@@ -115,8 +116,11 @@ Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
   int rows = page_few_rows((int64_t)s.max_q * s.G, dt);
   p.has_many = dt == SALSC_BF16 && (int64_t)s.max_q * s.G > rows;
   if (p.has_many) rows = page_few_rows(s.G, dt);
-  // page_few's counters come first: salsc_page_prepare clears them
+  // page_few's counters come first, and nothing else lies there whatever the
+  // descriptor: salsc_page_prepare clears them, and each call leaves them so
+  p.bytes = align_up(page_attend_cleared());
   p.few = layout(s, rows, page_few_grid(s, rows, dt), part, p.bytes);
+  p.few.done = (uint32_t*)part;
   p.few.tb = rows / s.G;
   p.few.over = kOverFew;
   p.few.min_rows = 1;
@@ -145,6 +149,8 @@ cudaError_t launch_merge(const PageStep& s, const PageWork& w, void* out, cudaSt
 
 }  // namespace
 
+size_t page_attend_cleared() { return sizeof(uint32_t) * 2 * kPageGrid; }
+
 size_t page_attend_workspace(const PageStep& s, salsc_dtype dt) {
   return make_plan(s, dt, nullptr).bytes;
 }
@@ -162,7 +168,5 @@ cudaError_t launch_page_attend(const PageStep& s, const void* q, int64_t q_strid
   if (p.has_many && e == cudaSuccess) e = launch_merge(s, p.many, out, stream);
   return e;
 }
-
-size_t page_attend_cleared() { return sizeof(uint32_t) * 2 * kPageGrid; }
 
 }  // namespace salsc

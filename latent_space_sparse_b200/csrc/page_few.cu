@@ -299,6 +299,9 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               if (s.rotate) page_cs(p0 + i, s.turns[e], c, sn);
               x2[j][0] = a * c - c2 * sn;
               x2[j][1] = c2 * c + a * sn;
+              // e4m3 has no infinity: NaN, as the scores would be
+              x2[j][0] += x2[j][0] - x2[j][0];
+              x2[j][1] += x2[j][1] - x2[j][1];
               amax = fmaxf(amax, fmaxf(fabsf(x2[j][0]), fabsf(x2[j][1])));
             }
           } else {
@@ -609,18 +612,14 @@ cudaError_t launch_d(int rc, const PageStep& s, const PageWork& w, const void* q
   switch (rc) {
     case 4: return launch<T, D, 4>(s, w, q, q_stride, kp, vp, ks, vs, out, stream);
     case 8: return launch<T, D, 8>(s, w, q, q_stride, kp, vp, ks, vs, out, stream);
-    case 16: return launch<T, D, 16>(s, w, q, q_stride, kp, vp, ks, vs, out, stream);
-    default:
-      if constexpr (sizeof(T) == 2)
-        return launch<T, D, 32>(s, w, q, q_stride, kp, vp, ks, vs, out, stream);
-      return cudaErrorInvalidConfiguration;
+    default: return launch<T, D, 16>(s, w, q, q_stride, kp, vp, ks, vs, out, stream);
   }
 }
 
 }  // namespace
 
 int page_few_rows(int64_t want, salsc_dtype dt) {
-  const int most = dt == SALSC_F32 ? 16 : 32;
+  const int most = 16;
   int rc = 4;
   while (rc < most && rc < want) rc *= 2;
   return rc;

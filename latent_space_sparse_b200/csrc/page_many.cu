@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // qexp [n_tokens][Hq].  A warp per token and kRotateHeads heads, whose rows it
 // loads at once; lanes hold two (d = 64: one) pairs, whose cos and sin serve
 // those heads.  Bound by memory: 2 bytes in, 2 out.  (A warp per token with
-// all its heads waited for four rows at a time: 18 against XXX us for 4096
+// all its heads waited for four rows at a time: it took longer: prompts of 4096
 // tokens of 32 heads.)
 constexpr int kRotateWarps = 8, kRotateHeads = 8;
 template <int D>
@@ -145,7 +145,7 @@ page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ P
   allow_dependent_launch();
   if (t >= s.n_tokens) return;
   // the last sequence whose first row is at or before t, by 32 tries at a time
-  int b = 0, n = s.B;
+  int b = s.offs ? 0 : min(t, s.B - 1), n = s.offs ? s.B : 1;
   while (n > 1) {
     const int step = (n + 31) / 32, k = b + lane * step;
     const bool at = k < b + n && (s.offs[k] <= t);

@@ -133,6 +133,15 @@ def test_attend_many_sequences():
     check_attend(Step(lens, [min(n, 1 + b % 3) for b, n in enumerate(lens)], 4, 2, 64, 16, seed=5))
 
 
+@pytest.mark.parametrize("single", [True, False])
+def test_very_many_sequences(single):
+    lens = [(b * 7) % 33 for b in range(2500)]
+    news = None if single else [min(n, b % 3) for b, n in enumerate(lens)]
+    s = Step(lens, news, 2, 1, 64, 16, seed=6)
+    check_attend(s)
+    check_append(s)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attend_one_long_sequence(dtype):
     check_attend(Step([20011], None, 8, 2, 128, 64, dtype, seed=6))
@@ -208,6 +217,34 @@ def test_attend_nan_in_the_cache_reaches_only_rows_that_see_it(news, dtype):
     assert torch.equal(got[~sees], ref[~sees])
     assert torch.equal(got[:, :g], ref[:, :g])
     assert torch.equal(got[:, 2 * g:], ref[:, 2 * g:])
+
+
+@pytest.mark.parametrize("news", [None, [3, 5], [90, 40]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_attend_query_that_is_not_finite_spoils_its_own_row_only(news, dtype, bad):
+    s = Step([150, 60], news, dtype=dtype, seed=32)
+    good = s.cache.attend(s.q, *s.pools)
+    q = s.q.clone()
+    q[1, 3, 10] = bad
+    out = s.cache.attend(q, *s.pools)
+    torch.cuda.synchronize()
+    assert out[1, 3].isnan().all()
+    out[1, 3], good[1, 3] = 0, 0
+    assert torch.equal(out, good)
+
+
+def test_one_workspace_for_steps_of_every_kind():
+    """Steps of different descriptors take turns with one workspace, in stream order."""
+    kinds = [Step([900, 33, 1], None, 8, 2, seed=41), Step([300, 500], [300, 9], 8, 2, seed=42),
+             Step([700, 40], [1, 7], 16, 1, dtype=F32, seed=43), Step([800], None, 4, 4, 64, 32, F32, seed=44),
+             Step([700, 20], [5, 3], 8, 2, seed=45)]
+    own = [s.cache.attend(s.q, *s.pools) for s in kinds]
+    most = max((s.cache for s in kinds), key=lambda c: c.ws.numel())
+    for _ in range(3):
+        for s, ref in zip(kinds, own):
+            s.cache._ws = most._ws
+            assert torch.equal(s.cache.attend(s.q, *s.pools), ref)
 
 
 def test_attend_strided_queries_of_a_fused_projection():
