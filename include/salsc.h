@@ -433,7 +433,9 @@ salsc_status salsc_shard_merge(const float* part_all, int32_t n_shards, int32_t 
  * outside 0 .. max_pages * page_size, offsets that decrease or pass n_tokens,
  * and more than max_q new tokens set bit 0 of the workspace's anomaly word;
  * tokens in a bad page are left out, lengths and offsets are cut to the
- * bounds, and rows past max_q are left as they were.
+ * bounds, and rows past max_q are left as they were (a row that two sequences
+ * claim belongs to either).  A wait inside a kernel that gives up sets bit 1;
+ * the step's outputs are then not valid.
  */
 typedef struct {
   int32_t batch;       /* B >= 1 */
@@ -462,7 +464,12 @@ typedef struct {
  */
 size_t salsc_page_workspace_size(const salsc_page_desc* desc);
 
-/* Clear the workspace's anomaly word (as salsc_decode_prepare); once per workspace. */
+/*
+ * Clear the workspace's anomaly word and the counters that the calls leave at
+ * zero; once per workspace, before its first call (and again after a call that
+ * set bit 1 of the anomaly word).  Descriptors of any kind may then take turns
+ * with the workspace, if it is large enough for each.
+ */
 salsc_status salsc_page_prepare(const salsc_page_desc* desc, void* ws, size_t ws_bytes,
                                 salsc_stream stream);
 
@@ -506,7 +513,16 @@ salsc_status salsc_page_append(const salsc_page_desc* desc, const void* K_new, i
  *   q    [n_tokens][Hq][d] before RoPE, rows q_stride elements apart (0:
  *        contiguous; otherwise a multiple of 8, at least Hq*d), 16-byte aligned
  *   out  [n_tokens][Hq][d] contiguous, 16-byte aligned, apart from the inputs
- * What lies in slots past a sequence's end does not matter (NaN included).
+ * What lies in slots past a sequence's end does not matter (NaN included).  A
+ * NaN or infinity in a query makes its row NaN; a NaN in a key or a scale that
+ * a row sees makes the row NaN, a NaN in a value at least that dimension of it.
+ * Scales may have any sign; they keep their accuracy from 2^-100 to 2^100.
+ *
+ * Accuracy: products of codes are exact and sums are fp32; fp32 storage keeps
+ * 24 bits of queries and weights, bf16 storage 11 or more (the output's own
+ * rounding is 2^-9).  The result of a call depends on the descriptor and the
+ * lengths, and is the same each time.
+ *
  * Allocates nothing, stream-ordered, graph-capturable; launched with
  * programmatic dependent launch, reading nothing before earlier work is done.
  * Errors: as salsc_page_append.

@@ -234,6 +234,47 @@ def test_attend_query_that_is_not_finite_spoils_its_own_row_only(news, dtype, ba
     assert torch.equal(out, good)
 
 
+@pytest.mark.parametrize("news", [None, [3, 5], [200, 40]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_scales_of_any_sign_and_zero(news, dtype):
+    s = Step([300, 60], news, dtype=dtype, seed=33)
+    g = torch.Generator(device=DEV).manual_seed(34)
+    for scales in s.pools[2:]:
+        scales *= torch.randint(-1, 2, scales.shape, generator=g, device=DEV)  # -1, 0, 1
+    check_attend(s)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("news", [None, [2], [260]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_scores_that_jump_by_thousands(news, dtype, d):
+    """Two tokens, each far above all before it: the row's result is the later one's value."""
+    n, page, first, second = 700, 16, 450, 600
+    s = Step([n], news, 4, 1, d, page, dtype, base=0.0, seed=35)
+    s.q.fill_(1.0)
+    codes = s.pools[0].view(torch.uint8)
+    codes.zero_()
+    s.pools[2].fill_(1.0)
+    for t, scale in ((first, 1.0), (second, 3.0)):
+        pg = int(s.table[0, t // page])
+        codes[pg, 0, t % page] = 0x7E  # 448
+        s.pools[2][pg] = scale
+    out = s.cache.attend(s.q, *s.pools)
+    torch.cuda.synchronize()
+    assert s.cache.flags() == 0
+    m = s.rows
+    vals = po.values(s.pools[1], s.pools[3])
+    for i in range(m):
+        pos = n - m + i
+        if pos < first:
+            continue  # all scores are zero
+        t = second if pos >= second else first
+        want = vals[s.table[0, t // page], 0, t % page]
+        got = out[i].double().cpu().numpy()
+        # the value's mantissa (24 bits of scale, 4 of code) in f16 or fp32, then the output's rounding
+        assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -10 if dtype == BF16 else 2.0 ** -22) * np.abs(want)).all()
+
+
 def test_one_workspace_for_steps_of_every_kind():
     """Steps of different descriptors take turns with one workspace, in stream order."""
     kinds = [Step([900, 33, 1], None, 8, 2, seed=41), Step([300, 500], [300, 9], 8, 2, seed=42),
