@@ -12,8 +12,10 @@
 // weights 11 bits.  Codes are read once per tile and both halves use them.
 //
 // Scales: a page's key scale multiplies its scores; its value scale
-// v = f * 2^e, 1 <= f < 2, enters the softmax as t = s + e (log2 units) and
-// the normaliser as p * 2^-e; f and both scales' signs go into the f16 values.
+// v = f * 2^e, 1 <= |f| < 2, enters the softmax as t = s + e (log2 units) and
+// the normaliser as p * 2^-e; f goes into the f16 values (nothing, and exact,
+// for the powers of two that the append writes; two roundings of 2^-12 for
+// others).
 // So the weights 2^(t - m) stay in f16's range whatever the scales are.
 //
 // The weights refer to a maximum that follows the rows' only when it must: a
@@ -30,6 +32,16 @@
 //
 // The queries are rotated by a kernel before (page_rotate_kernel): with a row
 // block's rotation inside the attention, every unit began with 25 us of it.
+//
+// What bounds it: a half's tile is a chain of scores (512 cycles of MMAs), their
+// load, 128 exponentials a thread (1024 cycles of the MUFU pipe if nobody else
+// asks) and values (512); two halves in flight cover each other only in part,
+// and a tile takes 4000 to 4200 cycles where the MMAs alone need 2048 and the
+// exponentials as much: MMA and MUFU pipes 52 % busy, issue slots 37 %.
+// Measured: 2048 tokens at the end of 32K, 32 heads on 8: 1.0 ms, 1.06 PFLOP/s.
+// Tried and slower: 16 softmax warps with two threads to a row (1.12 ms against
+// 1.08 then), scores by 64 tokens in turn (1.19 against 1.06), the halves taking
+// turns at the exponentials (1.16 against 1.06).
 #include "page.cuh"
 #include "tc.cuh"
 
@@ -37,6 +49,7 @@ namespace salsc {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kRegisters = 128; // a thread, at launch: shared out anew by the roles
 constexpr int kConvert = 128;   // threads of the converting warps
 constexpr int kRing = 4;        // tiles whose scales are kept
 constexpr float kMost = 256.f;  // sum of a tile's weights that the maximum must follow
@@ -130,9 +143,9 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // times a power of two for each row: qrot [n_tokens][Hq][d], exponents
 // qexp [n_tokens][Hq].  A warp per token and kRotateHeads heads, whose rows it
 // loads at once; lanes hold two (d = 64: one) pairs, whose cos and sin serve
-// those heads.  Bound by memory: 2 bytes in, 2 out.  (A warp per token with
-// all its heads waited for four rows at a time: it took longer: prompts of 4096
-// tokens of 32 heads.)
+// those heads.  Bound by memory: 2 bytes in, 2 out.  With a warp per token, four
+// of its rows at a time, a prompt of 4096 tokens and 32 heads took 227 us in all,
+// with this and page_merge_kernel's four rows a warp 216.
 constexpr int kRotateWarps = 8, kRotateHeads = 8;
 template <int D>
 __global__ void __launch_bounds__(kRotateWarps * 32)
@@ -272,7 +285,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       wait(segfull(i), (i / kSegments) & 1);
       return sh.segments[i % kSegments];
     };
-    // 200 * 256 + 64 * 128 + 48 * 128 = 128 * 512 registers
+    static_assert(200 * 256 + 64 * 128 + 48 * 128 == kRegisters * kThreads, "registers");
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
       // ------------------------------------------------ MMA issuer
@@ -743,6 +756,13 @@ cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t 
                    cudaStream_t stream) {
   static int done[kMaxDevices];
   auto kern = page_many_kernel<D>;
+  // The roles share out the registers that the block is launched with: a build
+  // that gave it fewer than they add up to would wait for them for good.
+  static const bool enough = [&] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == kRegisters;
+  }();
+  if (!enough) return cudaErrorInvalidConfiguration;
   cudaError_t e = ensure_smem(kern, Many<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap qm, km, vm;

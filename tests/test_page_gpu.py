@@ -537,6 +537,25 @@ def test_prompt_then_tokens_eager_graph_and_other_stream_agree(dtype):
         assert (np.abs(first[-1][i].double().cpu().numpy() - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_mixed_step_in_a_graph_serves_changing_lengths(dtype):
+    s = Step([700, 90, 400, 16], [300, 1, 40, 2], dtype=dtype, max_q=512, spare_rows=200, seed=51)
+    out = torch.zeros(s.rows, s.hq, s.d, dtype=dtype, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    s.cache.attend(s.q, *s.pools, out=out)
+    with torch.cuda.graph(g):
+        s.cache.append(s.K, s.V, *s.pools)
+        s.cache.attend(s.q, *s.pools, out=out)
+    for lens, news in (([700, 90, 400, 16], [300, 1, 40, 2]), ([650, 96, 1, 0], [500, 6, 1, 0]),
+                       ([33, 33, 33, 16], [1, 1, 1, 1])):
+        s.lens, s.news, s.offs = lens, news, np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        s.t_lens.copy_(torch.tensor(lens))
+        s.t_offs.copy_(torch.from_numpy(s.offs))
+        out.fill_(7.0)
+        g.replay()
+        check_attend(s, out)
+
+
 def test_two_caches_on_two_streams_at_once():
     a, b = Step([3000, 2000], None, seed=1), Step([900, 1200], [300, 250], seed=2)
     ra, rb = (s.cache.attend(s.q, *s.pools).clone() for s in (a, b))
