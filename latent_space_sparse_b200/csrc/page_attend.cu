@@ -6,7 +6,10 @@ namespace salsc {
 namespace {
 
 constexpr int kMergeWarps = 4, kMergeRows = 4;  // warps of a merge CTA, rows of a warp
-// What a unit takes besides its tiles, in tiles.
+// What a unit takes besides its tiles, in tiles: without it the CTAs with many
+// short units were last (a prompt of 4K 442 us, with it 261 at the time); 1, 2, 3,
+// 4 and 6 for page_few gave 67, 61, 53, 53 and 55 us on 64 short sequences, 2, 3,
+// 4, 6 and 8 for page_many 227, 227, 225, 228 and 232 us on a prompt of 4K.
 constexpr int kOverFew = 3, kOverMany = 3;
 
 // A warp takes kMergeRows rows of the unit that CTA c starts (usually of two

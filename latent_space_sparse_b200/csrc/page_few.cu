@@ -22,11 +22,21 @@
 // maximum keeps the weights within e4m3's range whatever the scales are.
 //
 // Work: tiles of 128 tokens of all units in one list, cut into equal ranges
-// for 148 persistent CTAs (page_sched.cuh); pieces of units that several CTAs
-// share leave (maximum, normaliser, sums), and the CTA whose piece is done last
-// merges them.
+// for two persistent CTAs per SM (page_sched.cuh); pieces of units that several
+// CTAs share leave (maximum, normaliser, sums), and the CTA whose piece is done
+// last merges them.
 // Warps: 0-3 softmax (a thread per token; in the epilogue per output
 // dimension), 4 TMA producer (lanes issue a tile's pages), 5 MMA issuer.
+//
+// What bounds it: long caches the read of the codes.  Single tokens of four
+// sequences of 32K (32 heads on 8): 51 us, 5.3 TB/s or 0.80 of the measured
+// copy rate; 16K to 128K: 84 us, 6.0 TB/s or 0.92.  The rest is about 9 us of
+// start and end: lengths, table, scales and codes one after another from
+// memory, the pipeline's first tile, and the merge.  With one CTA per SM (six
+// tiles in flight instead of three in each of two) 60 and 96 us, and 64 short
+// sequences 91 us instead of 53, for which the overlap of one CTA's unit
+// boundaries with the other's tiles counts most.  Short caches (4K tokens of 32
+// heads: 13 us; 8K tokens of fp32 storage: 14) are that chain.
 #include "page.cuh"
 #include "tc.cuh"
 
@@ -135,9 +145,9 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   }
   if (warp == 5) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
   if (warp == 4 && lane < 2) tc::tma_prefetch_desc(lane ? &vmap : &kmap);
-  // Behind page_many, which has waited for what came before it and runs on
-  // other sequences: this kernel's CTAs start where those have ended, and wait
-  // for all of them at their own end.
+  // Behind page_many, which runs on other sequences and starts when all that
+  // came before the step is done: this kernel's CTAs start where its CTAs have
+  // ended, and wait for all of them at their own end.
   if (!w.overlaps) grid_dependency_wait();
   allow_dependent_launch();
   tc::fence_before_sync();

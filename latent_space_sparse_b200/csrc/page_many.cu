@@ -266,7 +266,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   if (warp == 13 && lane < 3) tc::tma_prefetch_desc(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), C::kTmem);
   if (tid < 2 * kRing * 4) sh.nan[tid / 4][tid % 4] = 0;
-  grid_dependency_wait();
+  // The rotation before has waited for all that came before it, so only its own
+  // output is waited for: where queries are copied and where their exponents are
+  // read, and by all at the end (a kernel that waits for this one counts on it).
   allow_dependent_launch();
   if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc::fence_before_sync();
@@ -423,7 +425,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             __syncwarp();
             if (first && !dead) tc::tma_load_2d(dst, &kmap, 0, src, cfull(0));
             if (i == 0) {
-              if (seg > 0) wait(qfree, (seg - 1) & 1);
+              if (seg > 0)
+                wait(qfree, (seg - 1) & 1);
+              else
+                grid_dependency_wait();
               if (lane == 0) {
                 // whole boxes count, what lies behind the last row included
                 tc::mbar_expect_tx(qfull, dead ? 0u : (uint32_t)(2 * tb2 * s.G * D * 2));
@@ -575,6 +580,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       const uint32_t cs = lanes + h * 128, co = lanes + C::kColO + h * D;
       const int ri = r / s.G, rg = r - ri * s.G;  // token in the half, head in the group
       int cnt = 0;  // tiles of this half so far
+      grid_dependency_wait();  // the exponents
       for (int seg = 0;; ++seg) {
         const Segment& sg = segment(seg);
         const int n = dead ? 0 : sg.n;
@@ -748,6 +754,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   }
   __syncthreads();
   if (warp == 12) tc::tmem_dealloc(tmem, C::kTmem);
+  grid_dependency_wait();
 }
 
 template <int D>
