@@ -670,7 +670,8 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
                   lt = fmaf(sum0, mt.ive[k], lt);
                   tc::tmem_st8(cs + 8 * k, pk);  // the weights take the scores' place
                 }
-                if (last || !__any_sync(0xffffffffu, !(total < kMost) || m == -INFINITY)) break;
+                // (rows that do not exist may hold anything)
+                if (last || !__any_sync(0xffffffffu, live && (!(total < kMost) || m == -INFINITY))) break;
               }
               // go by this tile's maximum
               known = true;
