@@ -76,6 +76,12 @@ __device__ __forceinline__ int page_of(const PageStep& s, int b, int j) {
   return -1;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Two fp32 at a time.
 __device__ __forceinline__ void fma2(float& a0, float& a1, float m, float c) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"

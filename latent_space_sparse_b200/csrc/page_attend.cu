@@ -102,9 +102,9 @@ PageWork layout(const PageStep& s, int rows, int grid, void* part, size_t& off) 
 
 // The kernels of a step.  page_few takes sequences of up to 16 rows (new tokens
 // times heads per KV head) and all of fp32 storage, page_many the others: at 16
-// rows page_few takes 37 us and page_many 48 (16 sequences of 8192 tokens, 16
-// heads on one KV head), at 20 rows page_many 72 us and a page_few for 32 rows
-// 95 (4 sequences of 8192, 5 new tokens, 32 heads on 8).  A step that has both
+// rows page_few takes 62 us and page_many 83 (8 sequences of 8192 tokens, 4 of
+// them new, 32 heads on 8), at 20 rows page_many 49 us and a page_few for 32 rows
+// 95 (4 sequences of 8192, 5 new).  A step that has both
 // kinds sends page_few the sequences with a single new token only: its time
 // grows with the rows that it is built for (eight requests of 1 to 1024 new
 // tokens: 237 us with one for 32 rows, 208 with one for 4).

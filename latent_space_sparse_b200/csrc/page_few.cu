@@ -474,7 +474,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           if (grew) {
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
-              al[r] = al[r] == m[r] ? 1.f : exp2f(al[r] - m[r]);
+              al[r] = al[r] == m[r] ? 1.f : ex2(al[r] - m[r]);
               l[r] *= al[r];
             }
             if (i > 0) {  // the sums so far (of this piece) follow the maximum
@@ -495,26 +495,29 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           }
           if (it >= 2) wait(pvdone(buf), ((it - 2) >> 1) & 1);  // P's buffer is free
           unsigned char* dst = smem + C::kOffP + buf * kN * 128;
+          const float vfp = vf * kPScale;
 #pragma unroll
           for (int r = 0; r < RC; r += 2) {
-            float y[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float tt = t[r + k];
-              const float p = tt == -INFINITY ? 0.f : exp2f(tt - m[r + k]);
-              l[r + k] = fmaf(p, ive, l[r + k]);
-              y[k] = tt == -INFINITY ? 0.f : p * vf * kPScale;
+            // (a row that has seen nothing: its t are -inf, whatever they refer to)
+            const float p0 = ex2(t[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+            const float p1 = ex2(t[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]));
+            l[r] = fmaf(p0, ive, l[r]);
+            l[r + 1] = fmaf(p1, ive, l[r + 1]);
+            float y0 = p0 * vfp, y1 = p1 * vfp;
+            if (!full) {  // vf may be a NaN that not all rows see
+              y0 = t[r] == -INFINITY ? 0.f : y0;
+              y1 = t[r + 1] == -INFINITY ? 0.f : y1;
             }
 #pragma unroll
             for (int k = 0; k < kT; ++k) {
-              const uint32_t c = e4m3x2(y[0], y[1]);
+              const uint32_t c = e4m3x2(y0, y1);
               const int n0 = k * RC + r;
               dst[n0 * 128 + (tid ^ ((n0 & 7) << 4))] = (unsigned char)c;
               dst[(n0 + 1) * 128 + (tid ^ (((n0 + 1) & 7) << 4))] = (unsigned char)(c >> 8);
               if (k + 1 < kT) {
                 const float2 f = f32x2(c);
-                y[0] = (y[0] - f.x) * 16.f;
-                y[1] = (y[1] - f.y) * 16.f;
+                add2(y0, y1, -f.x, -f.y);
+                mul2(y0, y1, 16.f);
               }
             }
           }

@@ -99,12 +99,6 @@ struct Many {
   static constexpr int kColO = 256;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // 16 e4m3 codes -> 16 f16 in two chunks.
 __device__ __forceinline__ void widen16(const uint4& c, uint32_t (&w)[8]) {
   const uint32_t x[4] = {c.x, c.y, c.z, c.w};
