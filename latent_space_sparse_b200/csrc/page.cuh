@@ -82,6 +82,11 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// A byte of w is the NaN code 0x7F or 0xFF.
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
+
 // Two fp32 at a time.
 __device__ __forceinline__ void fma2(float& a0, float& a1, float m, float c) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"

@@ -97,11 +97,6 @@ __device__ __forceinline__ uint32_t add_acq_rel(uint32_t* p, uint32_t v) {
   return old;
 }
 
-// A byte of w is the NaN code 0x7F or 0xFF.
-__device__ __forceinline__ bool has_nan(uint32_t w) {
-  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
-}
-
 template <typename T, int D, int RC>
 __global__ void __launch_bounds__(kThreads, Few<T, D, RC>::kCtas)
 page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ PageWork w,

@@ -110,11 +110,6 @@ __device__ __forceinline__ void widen16(const uint4& c, uint32_t (&w)[8]) {
         : "r"(x[i]));
 }
 
-// A byte of w is the NaN code 0x7F or 0xFF.
-__device__ __forceinline__ bool has_nan(uint32_t w) {
-  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
-}
-
 // 32 bytes, the size of a sector: rows are apart, a thread has one to itself.
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
