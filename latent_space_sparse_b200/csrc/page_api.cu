@@ -52,10 +52,16 @@ salsc_status make_step(const salsc_page_desc* D, salsc::PageStep* S) {
   s.lens = D->seq_lens_dev;
   s.offs = D->q_offsets_dev;
   if (s.rotate) {
-    // products of the first power: 64 roundings of a 64-bit mantissa
-    const long double step = powl((long double)D->rope_base, -2.0L / s.d);
-    long double f = 0.159154943091895335768883763372514362L;
-    for (int i = 0; i < s.d / 2; ++i, f *= step) s.turns[i] = (uint64_t)(f * 18446744073709551616.0L + 0.5L);
+    // products of the first power in 64-bit fixed point: 64 roundings of 2^-64 of a
+    // turn, below 2^-27 of a turn at position 2^31
+    const long double two64 = 18446744073709551616.0L;
+    const long double step = powl((long double)D->rope_base, -2.0L / s.d) * two64;
+    const uint64_t step64 = step < two64 - 1.0L ? (uint64_t)step : UINT64_MAX;
+    uint64_t f = 0x28BE60DB9391054Aull;  // 1 / 2pi
+    for (int i = 0; i < s.d / 2; ++i) {
+      s.turns[i] = f;
+      f = (uint64_t)(((unsigned __int128)f * step64 + (1ull << 63)) >> 64);
+    }
   }
   *S = s;
   return SALSC_OK;

@@ -481,6 +481,7 @@ class PagedCache:
         self._held = (page_table, seq_lens, q_offsets)  # the descriptor points into them
         self.page_table, self.seq_lens, self.q_offsets = self._held
         self.device, self.dtype = page_table.device, dtype
+        self._dev = page_table.get_device()
         self.n_tokens = batch if n_tokens is None else int(n_tokens)
         self.kv_shape = (self.n_tokens, n_kv_heads, head_dim)
         self.q_shape = (self.n_tokens, n_q_heads, head_dim)
@@ -501,29 +502,34 @@ class PagedCache:
                    "salsc_page_prepare")
 
     def _rows(self, name, t, shape):
-        """Check a [n_tokens][heads][d] tensor; its row stride in elements."""
-        if t.dtype != self.dtype or t.device != self.device or t.shape != shape:
+        """Check a [n_tokens][heads][d] tensor; its row stride in elements (0: contiguous)."""
+        if t.dtype is not self.dtype or t.shape != shape or t.get_device() != self._dev:
             raise ValueError(f"{name} must be {self.dtype} {shape} on {self.device}")
+        if t.is_contiguous():
+            return 0
         stride = t.stride()
         if stride[2] != 1 or stride[1] != shape[2]:
             raise ValueError(f"{name}: the heads of a row must be contiguous")
         return stride[0] if shape[0] > 1 else 0
 
-    def _pools(self, pools):
-        dev = self.device.index
-        for i, t in enumerate(pools):
-            if (t.dtype is not (torch.float8_e4m3fn if i < 2 else torch.float32)
-                    or t.shape != (self.pool_shape if i < 2 else self.scale_shape)
-                    or t.get_device() != dev or not t.is_contiguous()):
-                raise ValueError(f"pools must be contiguous float8_e4m3fn {self.pool_shape}, twice, "
-                                 f"then float32 {self.scale_shape}, twice, on {self.device}")
-        return [t.data_ptr() for t in pools]
+    def _pools(self, k, v, ks, vs):
+        codes, scales, dev = self.pool_shape, self.scale_shape, self._dev
+        if not (k.dtype is torch.float8_e4m3fn and v.dtype is torch.float8_e4m3fn
+                and ks.dtype is torch.float32 and vs.dtype is torch.float32
+                and k.shape == codes and v.shape == codes
+                and ks.shape == scales and vs.shape == scales
+                and k.get_device() == dev and v.get_device() == dev
+                and ks.get_device() == dev and vs.get_device() == dev
+                and k.is_contiguous() and v.is_contiguous()
+                and ks.is_contiguous() and vs.is_contiguous()):
+            raise ValueError(f"pools must be contiguous float8_e4m3fn {codes}, twice, then float32 "
+                             f"{scales}, twice, on {self.device}")
 
     def _call(self, fn, what, stream, *args):
-        dev = self.device.index
-        if torch.cuda.current_device() == dev:
+        if torch.cuda.current_device() == self._dev:
             # the raw handle: a Stream object costs more than the launch
-            s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+            s = (torch._C._cuda_getCurrentRawStream(self._dev) if stream is None
+                 else stream.cuda_stream)
             st = fn(self._desc, *args, *self._ws, s)
         else:
             with torch.cuda.device(self.device):
@@ -535,21 +541,26 @@ class PagedCache:
     def append(self, K_new, V_new, k_pages, v_pages, k_scales, v_scales, stream=None):
         """Rotate, quantise and write this step's keys and values [n_tokens][n_kv_heads][d]
         (rows may be strided, as in a fused projection's output) into the pages."""
-        ks, vs = self._rows("K_new", K_new, self.kv_shape), self._rows("V_new", V_new, self.kv_shape)
-        self._call(_lib().salsc_page_append, "salsc_page_append", stream, K_new.data_ptr(), ks,
-                   V_new.data_ptr(), vs, *self._pools((k_pages, v_pages, k_scales, v_scales)))
+        k_stride = self._rows("K_new", K_new, self.kv_shape)
+        v_stride = self._rows("V_new", V_new, self.kv_shape)
+        self._pools(k_pages, v_pages, k_scales, v_scales)
+        self._call(_lib().salsc_page_append, "salsc_page_append", stream, K_new.data_ptr(),
+                   k_stride, V_new.data_ptr(), v_stride, k_pages.data_ptr(), v_pages.data_ptr(),
+                   k_scales.data_ptr(), v_scales.data_ptr())
 
     def attend(self, q, k_pages, v_pages, k_scales, v_scales, out=None, stream=None):
         """Attention of this step's queries [n_tokens][n_q_heads][d] (before RoPE; rows may be
         strided) over their sequences' pages; rows of no sequence are left as they were."""
-        qs = self._rows("q", q, self.q_shape)
+        q_stride = self._rows("q", q, self.q_shape)
+        self._pools(k_pages, v_pages, k_scales, v_scales)
         if out is None:
             out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
-        elif (out.dtype != self.dtype or out.device != self.device or out.shape != self.q_shape
-                or not out.is_contiguous()):
+        elif (out.dtype is not self.dtype or out.shape != self.q_shape
+                or out.get_device() != self._dev or not out.is_contiguous()):
             raise ValueError(f"out must be contiguous {self.dtype} {self.q_shape}")
-        self._call(_lib().salsc_page_attend, "salsc_page_attend", stream, q.data_ptr(), qs,
-                   *self._pools((k_pages, v_pages, k_scales, v_scales)), out.data_ptr())
+        self._call(_lib().salsc_page_attend, "salsc_page_attend", stream, q.data_ptr(), q_stride,
+                   k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                   v_scales.data_ptr(), out.data_ptr())
         return out
 
     def flags(self, stream=None) -> int:
