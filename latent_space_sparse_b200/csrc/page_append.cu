@@ -28,7 +28,7 @@
 // What bounds it: instructions, 60 % of the issue slots, then the latency of the
 // loads.  16.7K tokens of prompts (8 heads of 128, bf16): 27 us, 3.7 TB/s; with
 // sizes taken one by one and fp64 angles it was 47.  Single tokens: 3.5 us for 4
-// sequences of 8 heads, 8.8 for 64 of 32, one dependent load after another
+// sequences of 8 heads, 7.6 for 64 of 32, one dependent load after another
 // (lengths, table, the page's scale beside the new values).
 #include <algorithm>
 
@@ -38,7 +38,7 @@ namespace salsc {
 namespace {
 
 constexpr int kMinExp = -100;  // exponent of the scale of a page that holds only zeros
-constexpr int kTargetCtas = 8 * 148;  // small steps: about as many CTAs as run at once
+constexpr int kTargetCtas = 4 * 148;  // CTAs that run at once (64 registers of 256 threads each)
 
 // The least 2^e >= a / 448, e >= kMinExp (a finite, >= 0).  448 = 1.75 * 2^8.
 __device__ __forceinline__ float pow2_scale(float a) {
@@ -325,9 +325,10 @@ cudaError_t launch(const PageStep& s, const void* K, int64_t k_stride, const voi
   const int per = s.T * D / 32, items = kThreads / per, passes = (2 * s.U + items - 1) / items;
   // Passes of a CTA: so many that it computes one cos and sin a thread for
   // each (16.7K tokens, pages of 16: four passes 28.8 us, two 29.9, one 33.2);
-  // fewer where the step is small and CTAs would be missing.
+  // fewer where the step is small and CTAs would be missing (64 single tokens of
+  // 32 heads: two passes 7.6 us, one 8.9).
   int64_t part = std::max(1, s.T * (D / 2) / kThreads);
-  part = std::min(part, std::max<int64_t>(1, passes * pages / kTargetCtas));
+  part = std::min(part, std::max<int64_t>(1, (passes * pages + kTargetCtas - 1) / kTargetCtas));
   const int64_t parts = (passes + part - 1) / part;
   return launch_k(kern, dim3((unsigned)pages, (unsigned)parts), dim3(kThreads), smem, stream, true,
                   s, (const T*)K, k_stride, (const T*)V, v_stride, (uint8_t*)k_pages,

@@ -225,6 +225,12 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         }
         if (!cur.next_unit()) break;
       }
+      // given up: the copies in flight land before the block ends
+      if (__any_sync(0xffffffffu, dead))
+        for (int k = max(it - kStages, 0); k < it; ++k) {
+          tc::mbar_wait(kfull(k % kStages), (k / kStages) & 1, s.flags);
+          tc::mbar_wait(vfull(k % kStages), (k / kStages) & 1, s.flags);
+        }
     } else if (warp == 5) {
       // ------------------------------------------------ MMA issuer
       if (tc::elect_one()) {

@@ -437,6 +437,11 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             pg = pg_next;
             scales();
           }
+          // given up: the copies in flight land before the block ends
+          if (__any_sync(0xffffffffu, dead)) {
+            tc::mbar_wait(qfull, seg & 1, s.flags);
+            for (int v = 0; v < 2; ++v) tc::mbar_wait(cfull(v), (it - 1) & 1, s.flags);
+          }
           if (!cur.next_unit()) {
             if (lane == 0) {
               sh.segments[(seg + 1) % kSegments].n = 0;
