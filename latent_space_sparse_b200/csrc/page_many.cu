@@ -59,7 +59,7 @@ struct alignas(16) TileScales {  // read by float4
   float ks[8], ve[8], ive[8];  // key scale; value scale f * 2^e: e, 2^-e
   uint32_t vf[8];              // f, twice in f16
   uint32_t loaded;             // groups that were loaded (bits)
-  bool neg, plain;             // a key scale is negative; all f are 1
+  bool plain;                  // all f are 1
 };
 
 // A segment: a piece of one unit, this CTA's tiles of it.  Warp 13 writes them.
@@ -389,7 +389,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
             const int src = (pg * s.U + cur.u) * s.T;
             const uint32_t dst = sm0 + C::kOffCodes + lane * 16 * D;
-            const bool neg = __any_sync(0xffffffffu, ks < 0.f);
             // zeros and what is not finite keep e = 0
             int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
             if (e < -100 || e > 100) e = 0;
@@ -399,7 +398,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             if (lane == 0) {
               TileScales& mt = meta[it & (kRing - 1)];
               mt.loaded = loaded;
-              mt.neg = neg;
               mt.plain = plain;
             }
             if (lane < 8) {
@@ -595,11 +593,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const int64_t tile0 = (int64_t)(sg.t0 + i) * kPageTile;
             wait(sready(h), cnt & 1);
             tc::fence_after_sync();
-            // t = S * c + e by group of 16 tokens; where tokens are masked (or a key scale
-            // is negative) t itself takes S's place
+            // t = S * c + e by group of 16 tokens; where tokens are masked t itself takes
+            // S's place
             const uint32_t loaded = mt.loaded;
-            const bool masked =
-                !(tile0 >= sg.all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu) || mt.neg;
+            const bool masked = !(tile0 >= sg.all_lo && tile0 + kPageTile - 1 <= p0 && loaded == 0xFFu);
             if (masked) wait(vfull((it + i) & 1), ((it + i) >> 1) & 1);  // the NaN bits
             if (masked) {
               const int64_t top = min((int64_t)pos - tile0, (int64_t)kPageTile - 1);  // last token seen
