@@ -507,10 +507,13 @@ class PagedCache:
             raise ValueError(f"{name} must be {self.dtype} {shape} on {self.device}")
         if t.is_contiguous():
             return 0
+        rows, heads, d = shape
         stride = t.stride()
-        if stride[2] != 1 or stride[1] != shape[2]:
+        if stride[2] != 1 or (heads > 1 and stride[1] != d):
             raise ValueError(f"{name}: the heads of a row must be contiguous")
-        return stride[0] if shape[0] > 1 else 0
+        if rows > 1 and stride[0] < heads * d:  # expanded over the rows: 0 would mean contiguous
+            raise ValueError(f"{name}: rows must not overlap (stride {stride[0]} < {heads * d})")
+        return stride[0] if rows > 1 else 0
 
     def _pools(self, k, v, ks, vs):
         codes, scales, dev = self.pool_shape, self.scale_shape, self._dev

@@ -124,6 +124,32 @@ def test_binding_refuses_cpu_tensors():
         salsc.PagedCache(8, 2, 128, 16, 9, t.long(), torch.ones(2, dtype=torch.int32))
 
 
+def bare_cache(dtype=torch.bfloat16):
+    """A PagedCache's checks of its tensors, without a GPU."""
+    c = object.__new__(salsc.PagedCache)
+    c.dtype, c.device, c._dev = dtype, torch.device("cpu"), -1
+    return c
+
+
+def test_binding_refuses_rows_that_overlap():
+    """A row stride of 0 means contiguous to the entry points: rows expanded from one would be read
+    behind its end."""
+    c, shape = bare_cache(), (5, 4, 128)
+    one = torch.zeros(1, 4, 128, dtype=torch.bfloat16)
+    for bad in (one.expand(shape), torch.zeros(5 * 512, dtype=torch.bfloat16).as_strided(shape, (504, 128, 1))):
+        with pytest.raises(ValueError):
+            c._rows("q", bad, shape)
+    with pytest.raises(ValueError):  # expanded over the heads
+        c._rows("q", torch.zeros(5, 1, 128, dtype=torch.bfloat16).expand(shape), shape)
+    assert c._rows("q", one, (1, 4, 128)) == 0
+    assert c._rows("q", torch.zeros(shape, dtype=torch.bfloat16), shape) == 0
+    fused = torch.zeros(5, 12, 128, dtype=torch.bfloat16)
+    assert c._rows("K_new", fused[:, 4:8], shape) == 12 * 128
+    assert c._rows("K_new", fused[:, 4:5], (5, 1, 128)) == 12 * 128
+    # the stride of a single head does not matter
+    assert c._rows("K_new", fused.as_strided((5, 1, 128), (1536, 7, 1)), (5, 1, 128)) == 12 * 128
+
+
 # ---- oracle pins
 
 def test_oracle_code_table_is_e4m3():
