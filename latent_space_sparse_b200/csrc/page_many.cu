@@ -72,15 +72,17 @@ struct alignas(16) Segment {
   short u;      // KV head
   bool starts, whole;  // the unit's first tile is in the segment; all of them are
 };
-// A segment's entry is read until its last tile's results are out; the copying warp is at most
-// four tiles ahead of that.
+// An entry is read until its last tile's results are out. All readers say when they are done with
+// it, and the copying warp waits for that before it writes the entry again: the softmax warps of
+// the second half take part in no other barrier while units have one half only.
 constexpr int kSegments = 8;
+constexpr int kReaders = 13;  // warps: softmax 8, converting 4, MMA 1
 
 struct Shared {
   Segment segments[kSegments];
   TileScales meta[kRing];
   uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
-  uint64_t bars[20 + kSegments];
+  uint64_t bars[20 + 2 * kSegments];
   uint32_t tmem_base;
 };
 
@@ -234,6 +236,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   auto cfull = [&](int v) { return bar0 + 8u * (16 + v); };  // codes of K, of V
   auto cfree = [&](int v) { return bar0 + 8u * (18 + v); };
   auto segfull = [&](int i) { return bar0 + 8u * (20 + i % kSegments); };
+  auto segfree = [&](int i) { return bar0 + 8u * (20 + kSegments + i % kSegments); };
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -249,7 +252,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
     }
     tc::mbar_init(qfull, 1);
     tc::mbar_init(qfree, 1);
-    for (int i = 0; i < kSegments; ++i) tc::mbar_init(segfull(i), 1);
+    for (int i = 0; i < kSegments; ++i) {
+      tc::mbar_init(segfull(i), 1);
+      tc::mbar_init(segfree(i), kReaders);
+    }
     tc::mbar_fence_init();
   }
   if (warp == 13 && lane < 3) tc::tma_prefetch_desc(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
@@ -274,6 +280,14 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
     int it = 0;  // tiles so far
     auto segment = [&](int i) -> const Segment& {
       wait(segfull(i), (i / kSegments) & 1);
+      return sh.segments[i % kSegments];
+    };
+    auto read = [&](int i) {  // the warp is done with the entry
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(segfree(i));
+    };
+    auto writable = [&](int i) -> Segment& {
+      wait(segfree(i), ((i / kSegments) & 1) ^ 1);
       return sh.segments[i % kSegments];
     };
     static_assert(200 * 256 + 64 * 128 + 48 * 128 == kRegisters * kThreads, "registers");
@@ -314,6 +328,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           const int n = __shfl_sync(0xffffffffu, dead ? 0 : sg.n, 0);
           if (n == 0) break;
           const bool two = __shfl_sync(0xffffffffu, sg.p1 - sg.p0, 0) >= tb2;
+          read(seg);
           wait(qfull, seg & 1);
           wait(kfull(it & 1), (it >> 1) & 1);
           tc::fence_after_sync();
@@ -343,9 +358,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         const bool any = page_begin(cur, total, x1);
         for (int seg = 0;; ++seg) {
           const int n = any ? cur.upto(x1) : 0;
+          Segment& sg = writable(seg);
           if (n <= 0) {
             if (lane == 0) {
-              sh.segments[seg % kSegments].n = 0;
+              sg.n = 0;
               tc::mbar_arrive(segfull(seg));
             }
             break;
@@ -353,7 +369,6 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           const int t0 = cur.blk.tile0(cur.k) + cur.tile;
           const int p0 = cur.blk.pos0(cur.k), hi = cur.blk.pos1(cur.k), lo = cur.blk.lo(cur.k);
           if (lane == 0) {
-            Segment& sg = sh.segments[seg % kSegments];
             sg.n = n, sg.t0 = t0, sg.p0 = p0, sg.p1 = hi, sg.lo = lo;
             sg.all_lo = s.window ? (hi - p0 < s.window ? max(hi - s.window + 1, 0) : INT32_MAX) : 0;
             sg.row = cur.row0 + cur.k * w.tb;
@@ -441,8 +456,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             for (int v = 0; v < 2; ++v) tc::mbar_wait(cfull(v), (it - 1) & 1, s.flags);
           }
           if (!cur.next_unit()) {
+            Segment& end = writable(seg + 1);
             if (lane == 0) {
-              sh.segments[(seg + 1) % kSegments].n = 0;
+              end.n = 0;
               tc::mbar_arrive(segfull(seg + 1));
             }
             break;
@@ -535,6 +551,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         if (n == 0) break;
         const int p0 = sg.p0, p1 = sg.p1, lo = sg.lo, all_lo = sg.all_lo;
         const int64_t first = (int64_t)sg.t0 * kPageTile;
+        read(seg);
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it & 1;
           const int64_t tile0 = first + (int64_t)i * kPageTile;
@@ -741,6 +758,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           tc::fence_before_sync();
         }
         it += n;
+        read(seg);
       }
     }
   }

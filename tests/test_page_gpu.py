@@ -155,6 +155,15 @@ def test_attend_prompt_of_several_units_and_tiles_a_cta(lens, news, hq, hkv, d, 
     check_attend(Step(lens, news, hq, hkv, d, page, window=window, seed=8, page_gain=1.0))
 
 
+@pytest.mark.parametrize("hq,hkv,d,page", [(16, 16, 64, 16), (32, 8, 128, 32)])
+def test_attend_many_units_of_one_half_between_units_of_two(hq, hkv, d, page):
+    """Runs of units with at most 128 rows, more than a CTA keeps entries for, behind larger ones."""
+    g = hq // hkv
+    news = [200 // g if b % 40 == 0 else 5 + (b * 11) % (128 // g - 4 if b % 8 == 0 else 3) for b in range(160)]
+    lens = [m + (b * 29) % 150 for b, m in enumerate(news)]
+    check_attend(Step(lens, news, hq, hkv, d, page, seed=9))
+
+
 @pytest.mark.parametrize("window", [1, 2, 17, 100, 128, 129, 400])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attend_window(window, dtype):
