@@ -517,19 +517,23 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             c[k] = *(const uint4*)(smem + in + (k ? in1 : in0) + r0 * D);
             bad |= has_nan(c[k].x) || has_nan(c[k].y) || has_nan(c[k].z) || has_nan(c[k].w);
           }
+          uint32_t f = mt.vf[rr >> 4];
           if (!full) {
             // Rows differ in what they see.  A NaN would not be hidden by a
-            // weight of zero: such a token's values become zeros, and the NaN is
-            // handed to the rows that see it by their weights.
+            // weight of zero, nor would a factor that is not finite: such a token's
+            // values become zeros, and the NaN is handed to the rows that see it by
+            // their weights.
+            bad |= values && (f & 0x7C00u) == 0x7C00u;
             const int64_t tok = tile0 + rr;
             const bool none = tok < lo || tok > p1 || !((mt.loaded >> (rr >> 4)) & 1u);
             const uint32_t any = __ballot_sync(0xffffffffu, bad && !none) >> (lane & 28) & 15u;  // the row's lanes
-            if (none || (values && any))
+            if (none || (values && any)) {
 #pragma unroll
               for (int k = 0; k < kHalves; ++k) c[k] = make_uint4(0, 0, 0, 0);
+              f = 0x3C003C00u;  // 1
+            }
             if (values && any && col == 0) atomicOr(&nan[rr >> 5], 1u << (rr & 31));
           }
-          const uint32_t f = mt.vf[rr >> 4];
 #pragma unroll
           for (int k = 0; k < kHalves; ++k) {
             uint32_t x[8];

@@ -228,6 +228,27 @@ def test_attend_nan_in_the_cache_reaches_only_rows_that_see_it(news, dtype):
     assert torch.equal(got[:, 2 * g:], ref[:, 2 * g:])
 
 
+@pytest.mark.parametrize("news", [None, [3, 5], [150, 60], [290, 9]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 2.0 ** 119, 2.0 ** 127])
+def test_attend_scale_that_is_not_finite_reaches_only_rows_that_see_it(news, dtype, which, bad):
+    """A page's scale at the end of what a prompt holds: earlier rows of the same tile do not see it."""
+    s = Step([300, 60], news, dtype=dtype, seed=36)
+    first = 288  # sequence 0's last page
+    ref = s.cache.attend(s.q, *s.pools).clone()
+    s.pools[2 if which == "k" else 3][s.table[0, first // s.page], 1] = bad
+    got = s.cache.attend(s.q, *s.pools)
+    torch.cuda.synchronize()
+    sees = torch.tensor([i < s.news[0] and s.lens[0] - s.news[0] + i >= first for i in range(s.rows)])
+    g = s.hq // s.hkv
+    if bad != bad:
+        assert torch.isnan(got[sees][:, g:2 * g]).all()
+    assert torch.equal(got[~sees], ref[~sees])
+    assert torch.equal(got[:, :g], ref[:, :g])
+    assert torch.equal(got[:, 2 * g:], ref[:, 2 * g:])
+
+
 @pytest.mark.parametrize("news", [None, [3, 5], [90, 40]])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
