@@ -190,6 +190,8 @@ page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ P
       const float a = __uint_as_float(i ? xa[j] & 0xFFFF0000u : xa[j] << 16);
       const float b2 = __uint_as_float(i ? xb[j] & 0xFFFF0000u : xb[j] << 16);
       x[i] = a * c[i] - b2 * sn[i], y[i] = b2 * c[i] + a * sn[i];
+      // an infinity becomes NaN: scores of -inf alone would leave a row that sees nothing
+      x[i] += x[i] - x[i], y[i] += y[i] - y[i];
       am = fmaxf(am, fmaxf(fabsf(x[i]), fabsf(y[i])));
     }
     asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(am));
