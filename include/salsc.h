@@ -481,12 +481,13 @@ salsc_status salsc_page_prepare(const salsc_page_desc* desc, void* ws, size_t ws
  * position; |k| or |v| otherwise; values that are not finite do not count):
  *   scale = the least power of two with a <= 448 * scale (at least 2^-100);
  *           where the page holds earlier tokens (slots before the first new
- *           one), the larger of that and the page's scale
+ *           one), the larger of that and the size of the page's scale
  *   code  = the e4m3 number nearest to value / scale (ties to even;
  *           infinities become +-448, NaN stays)
- * Where the scale grew, the earlier tokens' codes are recoded with it; a power
- * of two only rounds those that fall below e4m3's normal range again.  Slots
- * behind the new tokens keep their bytes.
+ * Where the scale changed, the earlier tokens' codes are recoded with it, so that
+ * they keep what they stand for; a power of two only rounds those that fall
+ * below e4m3's normal range again.  If the page's scale was not finite, they
+ * become NaN and it does not count.  Slots behind the new tokens keep their bytes.
  *
  *   K_new, V_new  [n_tokens][Hkv][d], rows k_stride and v_stride elements
  *                 apart (0: contiguous; otherwise a multiple of 8, at least

@@ -7,8 +7,8 @@
 //           are rotated: it bounds sqrt(k_i^2 + k_{i+d/2}^2), which the
 //           rotation keeps, so the scale follows from the inputs alone and
 //           does not depend on how an angle rounds), or of |k|, |v|
-//   scale = 2^e, the least e with a <= 448 * 2^e, and no less than the page's
-//           scale where it holds earlier tokens
+//   scale = 2^e, the least e with a <= 448 * 2^e, and no less than the size of
+//           the page's scale where it holds earlier tokens
 //   code  = e4m3(x / scale)
 // A power of two costs e4m3 nothing (its relative step is the same at every
 // scale; at most one of its 16 binades is left unused) and makes growth cheap:
@@ -269,12 +269,16 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
       __syncwarp();
     }
     if (!live) continue;
+    // earlier codes stand for code * old: whatever its sign, they are recoded
+    // unless it stays (what is not finite becomes NaN)
     float sc = pow2_scale(a), ratio = 1.f;
-    if (old > 0.f && old <= 3.402823466e38f) {
-      ratio = old / sc;
-      if (ratio >= 1.f) {
-        sc = old;
-        ratio = 1.f;
+    if (lo > 0) {
+      const float size = fabsf(old);
+      if (size <= 3.402823466e38f) {
+        sc = fmaxf(sc, size);
+        ratio = old / sc;
+      } else {
+        ratio = __uint_as_float(0x7FC00000u);
       }
     }
     const float inv = 1.f / sc;

@@ -1,8 +1,10 @@
 """The paged 8-bit cache at the edges of what its calls take, against its definition in 64 bits
 (tests/page_oracle.py)."""
+import numpy as np
 import pytest
 import torch
 
+from tests import page_oracle as po
 from tests.test_page_gpu import BF16, F32, Step
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +26,39 @@ def test_attend_infinite_query_whose_scores_are_all_minus_infinity(dtype, news, 
     assert out[0, 5].isnan().all()
     out[0, 5], good[0, 5] = 0, 0
     assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("news", [None, [3, 5]])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("old", [-1.0, -0.25, 0.0, -2.0 ** 20, -3.0e-7, 2.0 ** 127, float("inf"),
+                                 float("-inf"), float("nan")])
+def test_append_behind_a_page_scale_of_any_kind_keeps_the_earlier_tokens(dtype, news, page, old):
+    """Earlier tokens keep what they stand for (code * scale); where that is not finite, NaN."""
+    lens = [page + 9, page + 12]
+    s = Step(lens, news, page=page, dtype=dtype, seed=38)
+    for b in range(2):
+        for scales in s.pools[2:]:
+            scales[s.table[b, 1]] = old
+    before = [p.clone() for p in s.pools]
+    s.cache.append(s.K, s.V, *s.pools)
+    torch.cuda.synchronize()
+    assert s.cache.flags() == 0
+    for x, pages, scales, p0, s0 in zip((s.K, s.V), s.pools[:2], s.pools[2:], before[:2], before[2:]):
+        x = x.double().cpu().numpy()
+        got, was = po.values(pages, scales), po.values(p0, s0)
+        for b, n in enumerate(lens):
+            m = s.news[b]
+            pg, lo = s.table[b, 1], n - m - page
+            size = np.abs(x[s.offs[b]:s.offs[b] + m])
+            if pages is s.pools[0]:
+                size = size[..., :s.d // 2] + size[..., s.d // 2:]
+            for u in range(s.hkv):
+                need = po.scale_for(size[:, u].max())
+                want = max(need, abs(old)) if np.isfinite(old) else need
+                assert float(scales[pg, u]) == want
+                a, e = got[pg, u, :lo], was[pg, u, :lo]
+                if np.isfinite(old):
+                    assert (np.abs(a - e) <= po.half_step(e, want)).all()
+                else:
+                    assert np.isnan(a).all()
