@@ -14,17 +14,20 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("news", [None, [100, 3], [4, 3]])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
 @pytest.mark.parametrize("code", [0x38, 0xB8])  # 1, -1
-def test_attend_infinite_query_whose_scores_are_all_minus_infinity(dtype, news, bad, code):
-    n0 = news[0] if news else 1
-    s = Step([n0, 60], news, dtype=dtype, base=0.0, seed=37)
-    s.pools[0].view(torch.uint8)[s.table[0, 0], 1, 0, 10] = code
+@pytest.mark.parametrize("pos,base", [(0, 0.0), (1, 0.0), (0, 10000.0), (1, 10000.0)])
+def test_attend_infinite_query_whose_scores_are_all_minus_infinity(dtype, news, bad, code, pos, base):
+    """(Away from position 0 the rotation spreads an infinity over its pair without making a NaN.)"""
+    n0 = news[0] if news else pos + 1
+    s = Step([n0, 60], news, dtype=dtype, base=base, seed=37)
+    row = pos if news else 0
+    s.pools[0].view(torch.uint8)[s.table[0, 0], 1, :pos + 1, 10::64] = code  # a pair of all that the row sees
     good = s.cache.attend(s.q, *s.pools)
     q = s.q.clone()
-    q[0, 5, 10] = bad  # row 0 sees token 0 only; head 5 reads KV head 1
+    q[row, 5, 10] = bad  # head 5 reads KV head 1
     out = s.cache.attend(q, *s.pools)
     torch.cuda.synchronize()
-    assert out[0, 5].isnan().all()
-    out[0, 5], good[0, 5] = 0, 0
+    assert out[row, 5].isnan().all()
+    out[row, 5], good[row, 5] = 0, 0
     assert torch.equal(out, good)
 
 
