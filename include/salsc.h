@@ -515,9 +515,13 @@ salsc_status salsc_page_append(const salsc_page_desc* desc, const void* K_new, i
  *        contiguous; otherwise a multiple of 8, at least Hq*d), 16-byte aligned
  *   out  [n_tokens][Hq][d] contiguous, 16-byte aligned, apart from the inputs
  * What lies in slots past a sequence's end does not matter (NaN included).  A
- * NaN or infinity in a query makes its row NaN; a NaN in a key or a scale that
- * a row sees makes the row NaN, a NaN in a value at least that dimension of it.
- * Scales may have any sign; they keep their accuracy from 2^-100 to 2^100.
+ * NaN or infinity in a query makes its row NaN; a NaN in a key, and a scale that
+ * is not finite, of tokens that a row sees make the row NaN, a NaN in a value at
+ * least that dimension of it.
+ * Scales may have any sign.  Value scales keep their accuracy from 2^-99 on, and
+ * beside each other in one row where they lie within 2^100; below 2^-99 values
+ * count as zeros, whose tokens keep their weight beside value scales from 2^-60
+ * to 2^50.
  *
  * Accuracy: products of codes are exact and sums are fp32; fp32 storage keeps
  * 24 bits of queries and weights, bf16 storage 11 or more (the output's own

@@ -158,6 +158,24 @@ __device__ __forceinline__ void page_cs(int pos, uint64_t turns, float& c, float
 
 // ---------------------------------------------------------------- attention
 
+// A page's value scale as f * 2^e.  Finite scales from 2^-99 on have 1 <= |f| < 2.
+// Smaller ones, which the append writes for pages of zeros, are zero beside
+// anything else: they take an e in the middle, so that such a page keeps its place
+// in the normaliser beside scales from 2^-60 to 2^50 and hides none of their values.
+// What is not finite is NaN.  down = 2^-e.
+struct ValueScale {
+  float f, e, down;
+};
+__device__ __forceinline__ ValueScale value_scale(float v) {
+  const int ex = (int)((__float_as_uint(v) >> 23) & 255u);
+  const int e = ex < 28 ? -50 : ex - 127;
+  const float down = __uint_as_float(e == 127 ? 0x00400000u : (uint32_t)(127 - e) << 23);
+  if (ex == 255) return ValueScale{__uint_as_float(0x7FC00000u), 0.f, 1.f};
+  return ValueScale{v * down, (float)e, down};
+}
+// A key scale: NaN if it is not finite, so that scores of -inf hide no token.
+__device__ __forceinline__ float key_scale(float k) { return k + (k - k); }
+
 // Which sequences a kernel of the attention takes, and how it cuts them.
 struct PageWork {
   int min_rows, max_rows;  // sequences with min_rows <= new tokens * G <= max_rows

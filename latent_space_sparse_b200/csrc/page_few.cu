@@ -201,14 +201,11 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               tc::tma_load_2d(dst + kTile, &vmap, 0, row, vfull(st));
             }
             if (mine) {
-              // value scale f * 2^e; zeros and what is not finite keep e = 0
-              int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
-              if (e < -100 || e > 100) e = 0;
-              const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-              meta[st].ks[sub] = ks;
-              meta[st].vf[sub] = vs * down;
-              meta[st].ve[sub] = (float)e;
-              meta[st].ive[sub] = down;
+              const ValueScale v = value_scale(vs);
+              meta[st].ks[sub] = key_scale(ks);
+              meta[st].vf[sub] = v.f;
+              meta[st].ve[sub] = v.e;
+              meta[st].ive[sub] = v.down;
               if (sub == 0) meta[st].loaded = got >> (npg * (i - i0));
             }
             __syncwarp();

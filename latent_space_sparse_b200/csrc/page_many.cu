@@ -406,11 +406,8 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
             const int src = (pg * s.U + cur.u) * s.T;
             const uint32_t dst = sm0 + C::kOffCodes + lane * 16 * D;
-            // zeros and what is not finite keep e = 0
-            int e = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
-            if (e < -100 || e > 100) e = 0;
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23), f = vs * down;
-            const bool plain = __all_sync(0xffffffffu, pg < 0 || f == 1.f);
+            const ValueScale v = value_scale(vs);
+            const bool plain = __all_sync(0xffffffffu, pg < 0 || v.f == 1.f);
             wait(cfree(0), (it & 1) ^ 1);
             if (lane == 0) {
               TileScales& mt = meta[it & (kRing - 1)];
@@ -419,10 +416,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             }
             if (lane < 8) {
               TileScales& mt = meta[it & (kRing - 1)];
-              mt.ks[lane] = ks;
-              mt.ve[lane] = (float)e;
-              mt.ive[lane] = down;
-              mt.vf[lane] = half2_bits(f, f);
+              mt.ks[lane] = key_scale(ks);
+              mt.ve[lane] = v.e;
+              mt.ive[lane] = v.down;
+              mt.vf[lane] = half2_bits(v.f, v.f);
             }
             __syncwarp();
             if (lane == 0) tc::mbar_expect_tx(cfull(0), bytes);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import page_oracle as po
-from tests.test_page_gpu import BF16, F32, Step
+from tests.test_page_gpu import BF16, DEV, F32, Step, check_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,22 @@ def test_append_behind_a_page_scale_of_any_kind_keeps_the_earlier_tokens(dtype, 
                     assert (np.abs(a - e) <= po.half_step(e, want)).all()
                 else:
                     assert np.isnan(a).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("news", [None, [3, 2], [150, 90]])
+@pytest.mark.parametrize("zero,rest", [(-100, 30), (-100, 50), (-100, -60), (-60, 40), (-99, 0), (119, 119),
+                                       (119, 20), (120, 120), (127, 127), (127, 30)])
+def test_attend_value_scales_far_apart(dtype, news, zero, rest):
+    """Pages of zeros beside pages of any magnitude (the append gives them a scale of 2^-100), and
+    value scales far from one."""
+    s = Step([200, 150], news, dtype=dtype, seed=39)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    small = torch.rand(s.n_pages, generator=g, device=DEV) < 0.5
+    s.pools[3] = torch.where(small[:, None], 2.0 ** zero, 2.0 ** rest).float().expand(-1, s.hkv).contiguous()
+    if zero == -100:
+        s.pools[1].view(torch.uint8)[small] = 0
+    if max(zero, rest) > 100:  # values that stay finite in bf16
+        top = 200.0 if zero < 127 else 1.5
+        s.pools[1] = s.pools[1].float().clamp(-top, top).to(torch.float8_e4m3fn)
+    check_attend(s)
