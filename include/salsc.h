@@ -523,10 +523,11 @@ salsc_status salsc_page_append(const salsc_page_desc* desc, const void* K_new, i
  * count as zeros, whose tokens keep their weight beside value scales from 2^-60
  * to 2^50.
  *
- * Accuracy: products of codes are exact and sums are fp32; fp32 storage keeps
- * 24 bits of queries and weights, bf16 storage 11 or more (the output's own
- * rounding is 2^-9).  The result of a call depends on the descriptor and the
- * lengths, and is the same each time.
+ * Accuracy: products of codes are exact and sums are fp32.  Of the elements of a
+ * query and of the weights of a row, fp32 storage keeps 24 bits, bf16 storage 11
+ * or more (the output's own rounding is 2^-9), where they are at least 2^-13 of
+ * the largest; smaller ones are off by up to 2^-42 and 2^-27 of it.  The result
+ * of a call depends on the descriptor and the lengths, and is the same each time.
  *
  * Allocates nothing, stream-ordered, graph-capturable; launched with
  * programmatic dependent launch, reading nothing before earlier work is done.

@@ -9,10 +9,13 @@
 // (TMA into shared memory, no conversion on the way):
 //   S^T [128 tokens x N] = K tile (M = tokens, K-major)  x  Q   (tcgen05 kind::f8f6f4)
 //   O^T [d x N]         += V tile (M = d, MN-major)      x  P
-// The other operand is cut into e4m3 terms, x = x0 + x1/16 + x2/256 + ...,
-// each the rounding of 16 times what the terms before it left: a term takes 4
+// The other operand is cut into e4m3 terms, x = x0 + x1/32 + x2/32^2 + ...,
+// each the rounding of 32 times what the terms before it left: a term takes 4
 // bits, the products are exact and the accumulators fp32.  3 terms hold 12
-// bits (relative 2^-12; bf16 storage has 8), 6 terms 24 (fp32 storage).  The
+// bits (relative 2^-12; bf16 storage has 8), 6 terms 24 (fp32 storage), of
+// numbers down to 2^-13 of the largest; of smaller ones what lies above 2^-27
+// (2^-42) of it.  (32 is the largest step whose terms stay below 448: a rounding
+// is off by 2^-5 of a number below 256.)  The
 // terms are columns of the same MMA (N = terms * RC), so they cost nothing
 // while N is small.
 //
@@ -46,6 +49,7 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kSoftmax = 128;
 constexpr float kPScale = 128.f;  // weights p * f <= 2 become <= 256
+constexpr float kStep = 32.f;     // a term counts 1 / kStep of the one before it
 constexpr int kMaxPages = 8;      // pages of a tile (page size >= 16)
 
 template <typename T>
@@ -338,8 +342,8 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               const int nrow = t * RC + r;
               dst[nrow * 128 + (e ^ ((nrow & 7) << 4))] = (unsigned char)c;
               dst[nrow * 128 + ((e + D / 2) ^ ((nrow & 7) << 4))] = (unsigned char)(c >> 8);
-              a = (a - f.x) * 16.f;
-              c2 = (c2 - f.y) * 16.f;
+              a = (a - f.x) * kStep;
+              c2 = (c2 - f.y) * kStep;
             }
           }
         }
@@ -384,7 +388,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
                 for (int k = kT - 1; k >= 0; --k) {
                   const int c = k * RC + r;
                   const float vv = __uint_as_float(c < 16 ? v[c] : v2[c - 16]);
-                  a = k == kT - 1 ? vv : fmaf(a, 0.0625f, vv);
+                  a = k == kT - 1 ? vv : fmaf(a, 1.f / kStep, vv);
                 }
                 t[r] = a;
               }
@@ -397,7 +401,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               for (int r = 0; r < kW; ++r) {
                 float a = __uint_as_float(v[kT - 1][r]);
 #pragma unroll
-                for (int k = kT - 2; k >= 0; --k) a = fmaf(a, 0.0625f, __uint_as_float(v[k][r]));
+                for (int k = kT - 2; k >= 0; --k) a = fmaf(a, 1.f / kStep, __uint_as_float(v[k][r]));
                 t[r0 + r] = a;
               }
             }
@@ -515,7 +519,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               if (k + 1 < kT) {
                 const float2 f = f32x2(c);
                 add2(y0, y1, -f.x, -f.y);
-                mul2(y0, y1, 16.f);
+                mul2(y0, y1, kStep);
               }
             }
           }
@@ -563,7 +567,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               if (r0 + r < rows) {
                 float a = __uint_as_float(v[kT - 1][r]);
 #pragma unroll
-                for (int k = kT - 2; k >= 0; --k) a = fmaf(a, 0.0625f, __uint_as_float(v[k][r]));
+                for (int k = kT - 2; k >= 0; --k) a = fmaf(a, 1.f / kStep, __uint_as_float(v[k][r]));
                 a *= 1.f / kPScale;
                 if (whole) {
                   const float ll = wsum[0][r0 + r] + wsum[1][r0 + r] + wsum[2][r0 + r] + wsum[3][r0 + r];

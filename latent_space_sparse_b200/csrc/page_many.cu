@@ -22,7 +22,10 @@
 // tile's weights are computed with what is at hand, and only if their sum
 // reaches kMost (none is larger then, and f16 holds them as well) computed again
 // with the tile's own maximum, when O is rescaled too.  So no maximum stands
-// between the scores and the exponentials of most tiles.
+// between the scores and the exponentials of most tiles.  What they refer to lies
+// 2^kUp below the maximum, in the middle between f16's largest number and kMost's
+// room to grow: weights keep 11 bits down to 2^-21 of the largest, and smaller
+// ones what lies above 2^-32 of it.
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of a half (a
 // thread per row), warps 8-11 cache tiles (codes to f16), warp 12 issues the
@@ -52,7 +55,8 @@ constexpr int kThreads = 512;
 constexpr int kRegisters = 128; // a thread, at launch: shared out anew by the roles
 constexpr int kConvert = 128;   // threads of the converting warps
 constexpr int kRing = 4;        // tiles whose scales are kept
-constexpr float kMost = 256.f;  // sum of a tile's weights that the maximum must follow
+constexpr float kUp = 7.f;        // log2 of the weight of the maximum that weights refer to
+constexpr float kMost = 32768.f;  // sum of a tile's weights that the maximum must follow
 
 // What the copying warp says of a tile, by group of 16 tokens.
 struct alignas(16) TileScales {  // read by float4
@@ -695,7 +699,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
                 for (int k = 0; k < 8; ++k) a[k] = max3(a[k], t[16 * k + j], t[16 * k + j + 1]);
               const float top = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
               const bool none = m == -INFINITY;
-              const float by = top > 0.f || (none && top > -INFINITY) ? top : 0.f;
+              const float by = top > kUp || (none && top > -INFINITY) ? top - kUp : 0.f;
               const float al = none ? 0.f : ex2(-by);
               if (!none || top > -INFINITY) m = (none ? 0.f : m) + by;
               l *= al;

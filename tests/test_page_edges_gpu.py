@@ -84,3 +84,35 @@ def test_attend_value_scales_far_apart(dtype, news, zero, rest):
         top = 200.0 if zero < 127 else 1.5
         s.pools[1] = s.pools[1].float().clamp(-top, top).to(torch.float8_e4m3fn)
     check_attend(s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("news", [None, [3], [100]])
+@pytest.mark.parametrize("times", [8.5, 10.5, 13.5, 20.3, 42.5])
+def test_attend_small_weights_beside_a_large_one(dtype, news, times):
+    """A first token that takes all the weight and has no value (a sink), and others at
+    times * 2^-24 of it, whose values are the result. (One tile: one maximum for all.)"""
+    n, d, far = 120, 128, 24 - np.log2(times)
+    s = Step([n], news, 4, 1, d, 64, dtype, base=0.0, seed=48)
+    s.q.fill_(1.0)
+    codes, values = (p.view(torch.uint8) for p in s.pools[:2])
+    codes.zero_()
+    first = int(s.table[0, 0])
+    codes[first, 0, 0] = 0x38  # 1: its score is sqrt(d) times its page's key scale
+    values[first, 0, 0] = 0
+    s.pools[2].fill_(1.0)
+    s.pools[2][first] = far * np.log(2.0) / np.sqrt(d)
+    s.pools[3].fill_(1.0)
+    values &= 0x7F  # positive: no cancellation
+    values.clamp_(max=0x40)  # at most 2
+    out = s.cache.attend(s.q, *s.pools).double().cpu().numpy()
+    step = dict(s.spec(), base=0.0)
+    ref, _ = po.attend(step, s.q, *s.pools, 4, dtype)
+    # a weight: its own floor, and the score's roundings (three factors and a sum at `far` log2
+    # units, each by half a step of 2^-23 relative); fp32 sums of 128 terms, twice; the
+    # output's rounding
+    floor, own = (2.0 ** -27, 2.0 ** -8) if dtype == BF16 else (2.0 ** -42, 2.0 ** -24)
+    rel = floor * 2.0 ** far + 4 * far * 2.0 ** -24 + 2 * 128 * 2.0 ** -24 + own
+    if dtype == BF16:
+        rel += 2.0 ** -11
+    assert (np.abs(out - ref) <= rel * np.abs(ref)).all(), np.max(np.abs(out - ref) / np.abs(ref)) / rel
