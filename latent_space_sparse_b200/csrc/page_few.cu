@@ -323,7 +323,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           amax = warp_max(amax);
           // power of two that brings the row's largest element into [128, 256)
           int ex = (int)(__float_as_uint(amax) >> 23) - 127 - 7;
-          ex = min(max(ex, -119), 119);
+          ex = max(ex, -119);
           const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
           if (lane == 0) {
             qfac[r] = s.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + ex) << 23);

@@ -201,7 +201,7 @@ page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ P
     asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(am));
     // power of two that brings the row's largest element into [2^7, 2^8)
     int ex = (int)(__float_as_uint(am) >> 23) - 127 - 7;
-    ex = min(max(ex, -119), 119);
+    ex = max(ex, -119);
     const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
     if (h < s.Hq) {
       if constexpr (kP == 2) {

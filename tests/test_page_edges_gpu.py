@@ -116,3 +116,11 @@ def test_attend_small_weights_beside_a_large_one(dtype, news, times):
     if dtype == BF16:
         rel += 2.0 ** -11
     assert (np.abs(out - ref) <= rel * np.abs(ref)).all(), np.max(np.abs(out - ref) / np.abs(ref)) / rel
+
+
+@pytest.mark.parametrize("news", [None, [3, 2], [40, 30]])
+def test_attend_queries_at_the_end_of_fp32(news):
+    s = Step([70, 50], news, dtype=F32, base=0.0, seed=40)
+    s.q *= 3.3e38 / s.q.abs().amax()
+    s.pools[2] *= 2.0 ** -123
+    check_attend(s)
