@@ -500,6 +500,9 @@ class PagedCache:
         with torch.cuda.device(self.device):
             _check(_lib().salsc_page_prepare(self._desc, *self._ws, _stream(None)),
                    "salsc_page_prepare")
+            # the calls may go to any stream, so the workspace is ready before the first of them
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     def _rows(self, name, t, shape):
         """Check a [n_tokens][heads][d] tensor; its row stride in elements (0: contiguous)."""

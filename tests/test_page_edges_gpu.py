@@ -124,3 +124,20 @@ def test_attend_queries_at_the_end_of_fp32(news):
     s.q *= 3.3e38 / s.q.abs().amax()
     s.pools[2] *= 2.0 ** -123
     check_attend(s)
+
+
+def test_constructor_is_ordered_before_calls_on_other_streams():
+    s = Step([3000, 2000], None, seed=45)
+    ref = s.cache.attend(s.q, *s.pools)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        junk = [torch.full((s.cache.ws.numel() + 256,), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
+        torch.cuda.synchronize()
+        del junk  # the next workspace's memory
+        torch.cuda._sleep(20_000_000)
+        cache = s.new_cache()
+        out = cache.attend(s.q, *s.pools, stream=side)
+        torch.cuda.synchronize()
+        assert cache.flags() == 0
+        assert torch.equal(out, ref)
