@@ -462,7 +462,9 @@ class PagedCache:
     with the same object, or a captured graph's next replay.  ``n_tokens`` is the number of rows
     of the step's tensors (default: batch), ``max_q`` the most new tokens of one sequence.
     The pools of a layer (alloc_pages) are passed per call: one object serves every layer, in
-    stream order.
+    stream order.  Calls go to the device's current stream, or to ``stream`` if one is given: it
+    must be ordered behind what made the tensors (``stream.wait_stream``), and an output that
+    ``attend`` allocates belongs to it.
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, page_table, seq_lens,
@@ -560,7 +562,11 @@ class PagedCache:
         q_stride = self._rows("q", q, self.q_shape)
         self._pools(k_pages, v_pages, k_scales, v_scales)
         if out is None:
-            out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
+            if stream is None:
+                out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
+            else:  # memory that the current stream may still be using is no place for its output
+                with torch.cuda.stream(stream):
+                    out = torch.empty(self.q_shape, dtype=self.dtype, device=self.device)
         elif (out.dtype is not self.dtype or out.shape != self.q_shape
                 or out.get_device() != self._dev or not out.is_contiguous()):
             raise ValueError(f"out must be contiguous {self.dtype} {self.q_shape}")

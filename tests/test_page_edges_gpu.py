@@ -141,3 +141,18 @@ def test_constructor_is_ordered_before_calls_on_other_streams():
         torch.cuda.synchronize()
         assert cache.flags() == 0
         assert torch.equal(out, ref)
+
+
+def test_output_allocated_for_a_stream_belongs_to_it():
+    s = Step([300, 200], None, seed=46)
+    ref = s.cache.attend(s.q, *s.pools)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        old = torch.empty_like(ref)
+        torch.cuda._sleep(20_000_000)
+        old.fill_(1.0)  # not done yet when its memory is free again
+        del old
+        out = s.cache.attend(s.q, *s.pools, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
