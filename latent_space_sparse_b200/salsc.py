@@ -534,6 +534,8 @@ class PagedCache:
                              f"{scales}, twice, on {self.device}")
 
     def _call(self, fn, what, stream, *args):
+        if stream is not None and stream.device_index != self._dev:
+            raise ValueError(f"stream must be on {self.device}")
         if torch.cuda.current_device() == self._dev:
             # the raw handle: a Stream object costs more than the launch
             s = (torch._C._cuda_getCurrentRawStream(self._dev) if stream is None

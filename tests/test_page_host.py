@@ -150,6 +150,16 @@ def test_binding_refuses_rows_that_overlap():
     assert c._rows("K_new", fused.as_strided((5, 1, 128), (1536, 7, 1)), (5, 1, 128)) == 12 * 128
 
 
+def test_binding_refuses_a_stream_of_another_device():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+
+    c = bare_cache()
+    c._dev = 0
+    with pytest.raises(ValueError):
+        c._call(None, "salsc_page_append", Stream())
+
+
 # ---- oracle pins
 
 def test_oracle_code_table_is_e4m3():
