@@ -460,7 +460,9 @@ class PagedCache:
     included) and ``q_offsets`` int32 [batch+1] (None: one new token of each sequence) are CUDA
     tensors that the calls read; writing new lengths and pages into them serves the next step
     with the same object, or a captured graph's next replay.  ``n_tokens`` is the number of rows
-    of the step's tensors (default: batch), ``max_q`` the most new tokens of one sequence.
+    of the step's tensors (default: batch), ``max_q`` the most new tokens of one sequence (default:
+    one, or with ``q_offsets`` as many as there are rows; a step of single tokens is faster with
+    ``max_q=1``).
     The pools of a layer (alloc_pages) are passed per call: one object serves every layer, in
     stream order.  Calls go to the device's current stream, or to ``stream`` if one is given: it
     must be ordered behind what made the tensors (``stream.wait_stream``), and an output that
@@ -468,7 +470,7 @@ class PagedCache:
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, page_table, seq_lens,
-                 q_offsets=None, n_tokens=None, max_q=1, rope_base=10000.0, softmax_scale=0.0,
+                 q_offsets=None, n_tokens=None, max_q=None, rope_base=10000.0, softmax_scale=0.0,
                  window=0, dtype=torch.bfloat16):
         batch, max_pages = page_table.shape
         for name, t, shape in (("page_table", page_table, (batch, max_pages)),
@@ -485,6 +487,8 @@ class PagedCache:
         self.device, self.dtype = page_table.device, dtype
         self._dev = page_table.get_device()
         self.n_tokens = batch if n_tokens is None else int(n_tokens)
+        if max_q is None:
+            max_q = 1 if q_offsets is None else self.n_tokens
         self.kv_shape = (self.n_tokens, n_kv_heads, head_dim)
         self.q_shape = (self.n_tokens, n_q_heads, head_dim)
         self.pool_shape = (n_pages, n_kv_heads, page_size, head_dim)

@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+from latent_space_sparse_b200 import salsc
 from tests import page_oracle as po
-from tests.test_page_gpu import BF16, DEV, F32, Step, check_attend
+from tests.test_page_gpu import BF16, DEV, F32, Step, check_append, check_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +157,12 @@ def test_output_allocated_for_a_stream_belongs_to_it():
         out = s.cache.attend(s.q, *s.pools, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("news", [None, [30, 1, 9]])
+def test_every_new_token_counts_where_max_q_is_not_given(news):
+    s = Step([40, 33, 9], news, seed=49)
+    s.cache = salsc.PagedCache(s.hq, s.hkv, s.d, s.page, s.n_pages, s.t_table, s.t_lens,
+                               None if s.single else s.t_offs, n_tokens=s.rows)
+    check_attend(s)
+    check_append(s)
