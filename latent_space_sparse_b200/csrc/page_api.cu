@@ -44,7 +44,7 @@ salsc_status make_step(const salsc_page_desc* D, salsc::PageStep* S) {
   s.n_pages = D->n_pages;
   s.max_pages = D->max_pages;
   s.n_tokens = D->n_tokens;
-  s.max_q = D->q_offsets_dev ? D->max_q : 1;
+  s.max_q = D->q_offsets_dev || D->max_q < 1 ? D->max_q : 1;
   s.window = D->window;
   s.rotate = D->rope_base != 0.0;
   s.scale = D->softmax_scale != 0.0f ? D->softmax_scale : (float)(1.0 / sqrt((double)s.d));

@@ -116,6 +116,12 @@ def test_nothing_to_do_is_ok_and_launches_nothing():
         assert attend(d) == OK
 
 
+def test_nothing_to_do_without_offsets():
+    d = desc(q_offsets_dev=None, max_q=0)
+    assert append(d) == OK
+    assert attend(d) == OK
+
+
 def test_binding_refuses_cpu_tensors():
     t = torch.zeros(2, 4, dtype=torch.int32)
     with pytest.raises(ValueError):
