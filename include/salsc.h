@@ -513,7 +513,8 @@ salsc_status salsc_page_append(const salsc_page_desc* desc, const void* K_new, i
  *
  *   q    [n_tokens][Hq][d] before RoPE, rows q_stride elements apart (0:
  *        contiguous; otherwise a multiple of 8, at least Hq*d), 16-byte aligned
- *   out  [n_tokens][Hq][d] contiguous, 16-byte aligned, apart from the inputs
+ *   out  [n_tokens][Hq][d] contiguous, 16-byte aligned, apart from the inputs (over
+ *        the rows of q: INVALID_ARG)
  * What lies in slots past a sequence's end does not matter (NaN included).  A
  * NaN or infinity in a query makes its row NaN; a NaN in a key, and a scale that
  * is not finite, of tokens that a row sees make the row NaN, a NaN in a value at

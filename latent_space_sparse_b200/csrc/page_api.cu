@@ -137,6 +137,12 @@ salsc_status salsc_page_attend(const salsc_page_desc* desc, const void* q, int64
       ((uintptr_t)k_scales & 3u) || ((uintptr_t)v_scales & 3u))
     return SALSC_ERR_INVALID_ARG;
   if (!fix_stride(q_stride, (int64_t)s.Hq * s.d)) return SALSC_ERR_INVALID_ARG;
+  if (s.n_tokens > 0) {  // pieces of a row's work read its queries after others wrote its output
+    const uintptr_t e = desc->dtype == SALSC_BF16 ? 2 : 4, row = (uintptr_t)s.Hq * s.d;
+    const uintptr_t q0 = (uintptr_t)q, q1 = q0 + ((uintptr_t)(s.n_tokens - 1) * q_stride + row) * e;
+    const uintptr_t o0 = (uintptr_t)out, o1 = o0 + (uintptr_t)s.n_tokens * row * e;
+    if (q0 < o1 && o0 < q1) return SALSC_ERR_INVALID_ARG;
+  }
   if ((st = check_ws(desc, s, ws, ws_bytes)) != SALSC_OK) return st;
   if (s.n_tokens == 0 || s.max_q == 0) return SALSC_OK;
   const cudaError_t e = salsc::launch_page_attend(s, q, q_stride, k_pages, v_pages, k_scales,

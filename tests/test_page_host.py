@@ -109,6 +109,16 @@ def test_attend_pointers_strides_workspace():
     assert attend(d, nb=size(d) - 1) == WORKSPACE
 
 
+def test_attend_refuses_an_output_over_its_queries():
+    """Pieces of a row's work read its queries when others may have written its output."""
+    d = desc()  # rows of 1024 bf16: 2048 bytes, 7 of them
+    q = 1 << 23
+    for out in (q, q + 16, q + 7 * 2048 - 16, q - 7 * 2048 + 16):
+        assert attend(d, q=q, out=out) == INVALID
+    for out in (q, q + 6 * 2560 + 2048 - 16):
+        assert attend(d, q=q, qs=1280, out=out) == INVALID
+
+
 def test_nothing_to_do_is_ok_and_launches_nothing():
     for kw in (dict(n_tokens=0), dict(max_q=0)):
         d = desc(**kw)
