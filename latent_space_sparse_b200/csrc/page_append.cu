@@ -181,7 +181,7 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
     const bool any = page_find(
         s.B,
         [&](int i) -> int64_t {
-          const PageSeq q = page_seq(s, i);
+          const PageSeq q = page_seq<false>(s, i);
           const int m = min(q.m, q.n);
           return m > 0 ? ((q.n - 1) >> s.log_t) - ((q.n - m) >> s.log_t) + 1 : 0;
         },
@@ -189,11 +189,11 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
     if (!any) return;
     j = (int)x;
   }
-  const PageSeq q = page_seq(s, b);
+  const PageSeq q = page_seq<false>(s, b);
   const int m = min(q.m, q.n), start = q.n - m;
   if (m <= 0) return;
   j += start >> s.log_t;
-  const int pg = page_of(s, b, j);
+  const int pg = page_of<false>(s, b, j);
   if (pg < 0) return;
   const int lo = max(start - j * s.T, 0), hi = min(q.n - j * s.T, s.T);  // new slots
   // row of slot 0 (may lie before the first new row)

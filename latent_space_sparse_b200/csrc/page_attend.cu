@@ -139,7 +139,6 @@ Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
     p.many.min_rows = rows + 1;
     p.many.max_rows = INT32_MAX;
     p.few.max_rows = rows;
-    p.few.overlaps = 1;
   }
   return p;
 }
@@ -162,10 +161,15 @@ cudaError_t launch_page_attend(const PageStep& s, const void* q, int64_t q_strid
                                const void* k_pages, const void* v_pages, const float* k_scales,
                                const float* v_scales, void* out, void* part, salsc_dtype dt,
                                cudaStream_t stream) {
-  const Plan p = make_plan(s, dt, part);
+  Plan p = make_plan(s, dt, part);
   cudaError_t e = cudaSuccess;
-  if (p.has_many)
+  if (p.has_many) {
     e = launch_page_many(s, p.many, q, q_stride, k_pages, v_pages, k_scales, v_scales, out, stream);
+    // page_few may begin beside page_many only right behind it: page_many begins when the
+    // rotation in front of it has waited for all earlier work, and page_few waits for both at
+    // its end, before anything that waits for page_few goes on
+    p.few.overlaps = 1;
+  }
   if (e == cudaSuccess)
     e = launch_page_few(s, p.few, q, q_stride, k_pages, v_pages, k_scales, v_scales, out, dt, stream);
   if (p.has_many && e == cudaSuccess) e = launch_merge(s, p.many, out, stream);

@@ -176,13 +176,13 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         auto look = [&](int tile) {
           const int64_t first = (int64_t)(t0 + tile) * kPageTile + (int64_t)lane * s.T;
           const bool need = tile + lane / npg < n && first <= hi && first + s.T > lo;
-          return need ? page_of(s, cur.b, (int)(first / s.T)) : -1;
+          return need ? page_of<true>(s, cur.b, (int)(first / s.T)) : -1;
         };
         int pg = look(0);
         float ks = 0.f, vs = 0.f;
         if (pg >= 0) {
-          ks = k_scales[(size_t)pg * s.U + cur.u];
-          vs = v_scales[(size_t)pg * s.U + cur.u];
+          ks = __ldcg(k_scales + (size_t)pg * s.U + cur.u);
+          vs = __ldcg(v_scales + (size_t)pg * s.U + cur.u);
         }
         for (int i0 = 0; i0 < n; i0 += per) {
           const int pg_n = i0 + per < n ? look(i0 + per) : -1;
@@ -190,8 +190,8 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           for (int i = i0; i < min(n, i0 + per); ++i, ++it) {
             const int st = it % kStages;
             if (i == min(n, i0 + per) - 1 && pg_n >= 0) {
-              ks_n = k_scales[(size_t)pg_n * s.U + cur.u];
-              vs_n = v_scales[(size_t)pg_n * s.U + cur.u];
+              ks_n = __ldcg(k_scales + (size_t)pg_n * s.U + cur.u);
+              vs_n = __ldcg(v_scales + (size_t)pg_n * s.U + cur.u);
             }
             wait(free_(st), ((it / kStages) & 1) ^ 1);
             const bool mine = lane / npg == i - i0;
@@ -306,7 +306,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
               const int e = lane + 32 * j;
-              const float a = to_f32(src[e]), c2 = to_f32(src[e + D / 2]);
+              const float a = to_f32(__ldcg(src + e)), c2 = to_f32(__ldcg(src + e + D / 2));
               float c = 1.f, sn = 0.f;
               if (s.rotate) page_cs(p0 + i, s.turns[e], c, sn);
               x2[j][0] = a * c - c2 * sn;

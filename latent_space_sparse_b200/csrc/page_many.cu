@@ -161,7 +161,7 @@ page_rotate_kernel(const __grid_constant__ PageStep s, const __grid_constant__ P
     n = min(step, n - hit * step);
     b += hit * step;
   }
-  const PageSeq sq = page_seq(s, b);
+  const PageSeq sq = page_seq<false>(s, b);
   const int64_t rows = (int64_t)sq.m * s.G;
   if (rows < w.min_rows || rows > w.max_rows || t < sq.row0 || t >= sq.row0 + sq.m) return;
   const int pos = sq.n - sq.m + (t - sq.row0);
@@ -267,9 +267,10 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   if (warp == 13 && lane < 3) tc::tma_prefetch_desc(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), C::kTmem);
   if (tid < 2 * kRing * 4) sh.nan[tid / 4][tid % 4] = 0;
-  // The rotation before has waited for all that came before it, so only its own
-  // output is waited for: where queries are copied and where their exponents are
-  // read, and by all at the end (a kernel that waits for this one counts on it).
+  // page_rotate_kernel, launched right before, has waited for all that came before
+  // it, so only its own output is waited for: where queries are copied and where
+  // their exponents are read, and by all at the end (a kernel that waits for this
+  // one counts on it).  What is read earlier comes past L1.
   allow_dependent_launch();
   if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc::fence_before_sync();
@@ -390,15 +391,15 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           // whole if a row sees any of it
           auto look = [&](int i) {
             const int64_t first = (int64_t)(t0 + i) * kPageTile + ((lane & 7) * 16 & -s.T);
-            return i < n && first <= hi && first + s.T > lo ? page_of(s, cur.b, (int)(first / s.T)) : -1;
+            return i < n && first <= hi && first + s.T > lo ? page_of<true>(s, cur.b, (int)(first / s.T)) : -1;
           };
           int pg = look(0);
           float ks = 0.f, vs = 0.f;
           auto scales = [&] {
             ks = vs = 0.f;
             if (pg >= 0) {
-              ks = k_scales[(size_t)pg * s.U + cur.u];
-              vs = v_scales[(size_t)pg * s.U + cur.u];
+              ks = __ldcg(k_scales + (size_t)pg * s.U + cur.u);
+              vs = __ldcg(v_scales + (size_t)pg * s.U + cur.u);
             }
           };
           scales();
@@ -794,6 +795,8 @@ cudaError_t launch(const PageStep& s, const PageWork& w, const void* q, int64_t 
   if (!make_tmap_f16_heads(&qm, w.qrot, s.n_tokens, s.Hq, D, w.tb / 2, s.G) ||
       !make_tmap_u8_rows(&km, kp, rows, D, s.T) || !make_tmap_u8_rows(&vm, vp, rows, D, s.T))
     return cudaErrorInvalidValue;
+  // these two in this order, and nothing between them: page_many_kernel counts on
+  // the rotation's wait for all earlier work
   e = launch_k(page_rotate_kernel<D>, dim3((unsigned)((s.n_tokens + kRotateWarps - 1) / kRotateWarps),
                     (unsigned)((s.Hq + kRotateHeads - 1) / kRotateHeads)),
                dim3(kRotateWarps * 32), 0, stream, true, s, w, (const __nv_bfloat16*)q, q_stride);

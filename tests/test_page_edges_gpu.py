@@ -166,3 +166,20 @@ def test_every_new_token_counts_where_max_q_is_not_given(news):
                                None if s.single else s.t_offs, n_tokens=s.rows)
     check_attend(s)
     check_append(s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("hq,hkv,news", [(8, 2, None), (32, 32, None), (8, 8, [60, 1, 1, 9, 1, 33] * 5),
+                                         (32, 8, [60, 1, 1, 9, 1, 33] * 5)])
+def test_attend_right_behind_an_append_reads_what_it_wrote(dtype, hq, hkv, news):
+    """Scales of a page's heads lie side by side and are written by different CTAs; each step lets
+    the last pages' scales grow."""
+    lens = [(37 * b) % 200 + 61 for b in range(30)]
+    s = Step(lens, news, hq, hkv, 64, 128, dtype, seed=47)
+    pools = [p.clone() for p in s.pools]
+    for i in range(12):
+        K, V = s.K * 1.9 ** i, s.V * 1.9 ** i
+        s.cache.append(K, V, *pools)
+        got = s.cache.attend(s.q, *pools)
+        torch.cuda.synchronize()
+        assert torch.equal(got, s.cache.attend(s.q, *pools)), i
