@@ -148,10 +148,10 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   // came before the step is done: this kernel's CTAs start where its CTAs have
   // ended, and wait for all of them at their own end.
   if (!w.overlaps) grid_dependency_wait();
-  allow_dependent_launch();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  allow_dependent_launch();  // (a kernel that uses tensor memory must not come first to it)
   const uint32_t tmem = tmem_base;
   bool dead = false;  // a wait gave up: skip the others, so that the kernel ends
   auto wait = [&](uint32_t bar, uint32_t parity) {

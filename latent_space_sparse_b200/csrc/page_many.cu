@@ -271,11 +271,11 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   // it, so only its own output is waited for: where queries are copied and where
   // their exponents are read, and by all at the end (a kernel that waits for this
   // one counts on it).  What is read earlier comes past L1.
-  allow_dependent_launch();
   if (tid == 0) w.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  allow_dependent_launch();  // (a kernel that uses tensor memory must not come first to it)
   const uint32_t tmem = sh.tmem_base;
   bool dead = false;  // a wait gave up: skip the others, so that the kernel ends
   auto wait = [&](uint32_t bar, uint32_t parity) {
