@@ -111,7 +111,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   constexpr int kN = C::kN, kStages = C::kStages, kTile = C::kTileBytes, kT = kTerms<T>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ TileMeta meta[kStages];
-  __shared__ alignas(8) uint64_t bars[3 * kStages + 7];
+  __shared__ alignas(8) uint64_t bars[3 * kStages + 8];
   __shared__ alignas(16) float wmax[2][4][RC];
   __shared__ alignas(16) float wsum[4][RC];
   __shared__ float qfac[RC];     // softmax scale * log2(e) / the row's power of two
@@ -130,7 +130,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
   auto sready = [&](int i) { return bar0 + 8u * (3 * kStages + i); };
   auto pready = [&](int i) { return bar0 + 8u * (3 * kStages + 2 + i); };
   auto pvdone = [&](int i) { return bar0 + 8u * (3 * kStages + 4 + i); };
-  const uint32_t qready = bar0 + 8u * (3 * kStages + 6);
+  const uint32_t qready = bar0 + 8u * (3 * kStages + 6), drained = bar0 + 8u * (3 * kStages + 7);
 
   if (tid == 0) {
     for (int i = 0; i < 3 * kStages; ++i) tc::mbar_init(bar0 + 8u * i, 1);
@@ -140,6 +140,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
       tc::mbar_init(pvdone(i), 1);
     }
     tc::mbar_init(qready, kSoftmax);
+    tc::mbar_init(drained, 1);
     tc::mbar_fence_init();
   }
   if (warp == 5) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
@@ -166,7 +167,8 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
 
     if (warp == 4) {
       // ------------------------------------------------ TMA producer
-      while (true) {
+      bool gone = false;  // a lane gave up: the warp stops
+      while (!gone) {
         const int n = cur.upto(x1);
         if (n <= 0) break;
         const int t0 = cur.blk.tile0(cur.k) + cur.tile;
@@ -184,7 +186,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           ks = __ldcg(k_scales + (size_t)pg * s.U + cur.u);
           vs = __ldcg(v_scales + (size_t)pg * s.U + cur.u);
         }
-        for (int i0 = 0; i0 < n; i0 += per) {
+        for (int i0 = 0; i0 < n && !gone; i0 += per) {
           const int pg_n = i0 + per < n ? look(i0 + per) : -1;
           float ks_n = 0.f, vs_n = 0.f;
           for (int i = i0; i < min(n, i0 + per); ++i, ++it) {
@@ -194,11 +196,12 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               vs_n = __ldcg(v_scales + (size_t)pg_n * s.U + cur.u);
             }
             wait(free_(st), ((it / kStages) & 1) ^ 1);
+            if ((gone = __any_sync(0xffffffffu, dead))) break;
             const bool mine = lane / npg == i - i0;
             const int sub = lane % npg;
             const uint32_t got = __ballot_sync(0xffffffffu, mine && pg >= 0);
             // the copies first: the scales may still be on their way
-            if (mine && pg >= 0 && !dead) {
+            if (mine && pg >= 0) {
               const uint32_t dst = sm0 + (uint32_t)st * 2 * kTile + (uint32_t)sub * s.T * D;
               const int row = (pg * s.U + cur.u) * s.T;
               tc::tma_load_2d(dst, &kmap, 0, row, kfull(st));
@@ -213,7 +216,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               if (sub == 0) meta[st].loaded = got >> (npg * (i - i0));
             }
             __syncwarp();
-            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine && pg >= 0 && !dead)) * s.T * D;
+            const uint32_t bytes = (uint32_t)__popc(got) * s.T * D;
             if (lane == 0) {
               tc::mbar_expect_tx(kfull(st), bytes);
               tc::mbar_expect_tx(vfull(st), bytes);
@@ -226,8 +229,8 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         }
         if (!cur.next_unit()) break;
       }
-      // given up: the copies in flight land before the block ends
-      if (__any_sync(0xffffffffu, dead))
+      // the copies in flight land before the block ends
+      if (gone)
         for (int k = max(it - kStages, 0); k < it; ++k) {
           tc::mbar_wait(kfull(k % kStages), (k / kStages) & 1, s.flags);
           tc::mbar_wait(vfull(k % kStages), (k / kStages) & 1, s.flags);
@@ -278,6 +281,10 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
             values(it, i == 0);
           }
           if (!cur.next_unit()) break;
+        }
+        if (dead) {  // and so do the MMAs, before tensor memory is given back
+          tc::mma_commit(drained);
+          tc::mbar_wait(drained, 0, s.flags);
         }
       }
       __syncwarp();

@@ -86,7 +86,7 @@ struct Shared {
   Segment segments[kSegments];
   TileScales meta[kRing];
   uint32_t nan[2 * kRing][4];  // tokens whose values hold a NaN, where rows differ in what they see
-  uint64_t bars[20 + 2 * kSegments];
+  uint64_t bars[21 + 2 * kSegments];
   uint32_t tmem_base;
 };
 
@@ -242,6 +242,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
   auto cfull = [&](int v) { return bar0 + 8u * (16 + v); };  // codes of K, of V
   auto cfree = [&](int v) { return bar0 + 8u * (18 + v); };
   auto segfull = [&](int i) { return bar0 + 8u * (20 + i % kSegments); };
+  const uint32_t drained = bar0 + 8u * (20 + 2 * kSegments);
   auto segfree = [&](int i) { return bar0 + 8u * (20 + kSegments + i % kSegments); };
 
   if (tid == 0) {
@@ -258,6 +259,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
     }
     tc::mbar_init(qfull, 1);
     tc::mbar_init(qfree, 1);
+    tc::mbar_init(drained, 1);
     for (int i = 0; i < kSegments; ++i) {
       tc::mbar_init(segfull(i), 1);
       tc::mbar_init(segfree(i), kReaders);
@@ -289,6 +291,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       wait(segfull(i), (i / kSegments) & 1);
       return sh.segments[i % kSegments];
     };
+    auto gone = [&] { return (bool)__any_sync(0xffffffffu, dead); };  // a lane gave up: the warp stops
     auto read = [&](int i) {  // the warp is done with the entry
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(segfree(i));
@@ -332,7 +335,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
         };
         for (int seg = 0;; ++seg) {
           const Segment& sg = segment(seg);
-          const int n = __shfl_sync(0xffffffffu, dead ? 0 : sg.n, 0);
+          const int n = gone() ? 0 : __shfl_sync(0xffffffffu, sg.n, 0);
           if (n == 0) break;
           const bool two = __shfl_sync(0xffffffffu, sg.p1 - sg.p0, 0) >= tb2;
           read(seg);
@@ -357,15 +360,21 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             }
           }
         }
+        if (gone()) {  // the MMAs in flight end before tensor memory is given back
+          tc::commit_lead(lead, drained);
+          tc::mbar_wait(drained, 0, s.flags);
+        }
       }
       // ------------------------------------------------ pages to shared memory
       if (warp == 13) {
         PageCursor cur(s, w);
         int64_t total, x1;
         const bool any = page_begin(cur, total, x1);
-        for (int seg = 0;; ++seg) {
+        int nk = 0, nv = 0, nq = 0;  // copies of K, V and queries
+        for (int seg = 0; !gone(); ++seg) {
           const int n = any ? cur.upto(x1) : 0;
           Segment& sg = writable(seg);
+          if (gone()) break;
           if (n <= 0) {
             if (lane == 0) {
               sg.n = 0;
@@ -406,7 +415,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
           for (int i = 0; i < n; ++i, ++it) {
             const int pg_next = look(i + 1);
             const uint32_t loaded = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
-            const uint32_t bytes = dead ? 0u : (uint32_t)__popc(loaded) * 16 * D;
+            const uint32_t bytes = (uint32_t)__popc(loaded) * 16 * D;
             // a page's first group copies it (a tile holds whole pages)
             const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
             const int src = (pg * s.U + cur.u) * s.T;
@@ -414,6 +423,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const ValueScale v = value_scale(vs);
             const bool plain = __all_sync(0xffffffffu, pg < 0 || v.f == 1.f);
             wait(cfree(0), (it & 1) ^ 1);
+            if (gone()) break;
             if (lane == 0) {
               TileScales& mt = meta[it & (kRing - 1)];
               mt.loaded = loaded;
@@ -429,44 +439,47 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             __syncwarp();
             if (lane == 0) tc::mbar_expect_tx(cfull(0), bytes);
             __syncwarp();
-            if (first && !dead) tc::tma_load_2d(dst, &kmap, 0, src, cfull(0));
+            if (first) tc::tma_load_2d(dst, &kmap, 0, src, cfull(0));
+            ++nk;
             if (i == 0) {
               if (seg > 0)
                 wait(qfree, (seg - 1) & 1);
               else
                 grid_dependency_wait();
+              if (gone()) break;
               if (lane == 0) {
                 // whole boxes count, what lies behind the last row included
-                tc::mbar_expect_tx(qfull, dead ? 0u : (uint32_t)(2 * tb2 * s.G * D * 2));
-                if (!dead)
-                  for (int j = 0; j < 2 * (D / 64); ++j)
-                    tc::tma_load_3d(sm0 + j * 16384, &qmap, j % (D / 64) * 64, cur.u * s.G,
-                                    cur.row0 + cur.k * w.tb + j / (D / 64) * tb2, qfull);
+                tc::mbar_expect_tx(qfull, (uint32_t)(2 * tb2 * s.G * D * 2));
+                for (int j = 0; j < 2 * (D / 64); ++j)
+                  tc::tma_load_3d(sm0 + j * 16384, &qmap, j % (D / 64) * 64, cur.u * s.G,
+                                  cur.row0 + cur.k * w.tb + j / (D / 64) * tb2, qfull);
               }
               __syncwarp();
+              ++nq;
             }
             wait(cfree(1), (it & 1) ^ 1);
+            if (gone()) break;
+            if (lane == 0) tc::mbar_expect_tx(cfull(1), bytes);
             __syncwarp();
-            const uint32_t vbytes = __any_sync(0xffffffffu, dead) ? 0u : bytes;
-            if (lane == 0) tc::mbar_expect_tx(cfull(1), vbytes);
-            __syncwarp();
-            if (first && vbytes) tc::tma_load_2d(dst + C::kCodeBytes, &vmap, 0, src, cfull(1));
+            if (first) tc::tma_load_2d(dst + C::kCodeBytes, &vmap, 0, src, cfull(1));
+            ++nv;
             pg = pg_next;
             scales();
           }
-          // given up: the copies in flight land before the block ends
-          if (__any_sync(0xffffffffu, dead)) {
-            tc::mbar_wait(qfull, seg & 1, s.flags);
-            for (int v = 0; v < 2; ++v) tc::mbar_wait(cfull(v), (it - 1) & 1, s.flags);
-          }
+          if (gone()) break;
           if (!cur.next_unit()) {
             Segment& end = writable(seg + 1);
-            if (lane == 0) {
+            if (lane == 0 && !dead) {
               end.n = 0;
               tc::mbar_arrive(segfull(seg + 1));
             }
             break;
           }
+        }
+        if (gone()) {  // the copies in flight land before the block ends
+          if (nk) tc::mbar_wait(cfull(0), (nk - 1) & 1, s.flags);
+          if (nv) tc::mbar_wait(cfull(1), (nv - 1) & 1, s.flags);
+          if (nq) tc::mbar_wait(qfull, (nq - 1) & 1, s.flags);
         }
       }
       __syncwarp();
@@ -555,7 +568,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       };
       for (int seg = 0;; ++seg) {
         const Segment& sg = segment(seg);
-        const int n = dead ? 0 : sg.n;
+        const int n = gone() ? 0 : sg.n;
         if (n == 0) break;
         const int p0 = sg.p0, p1 = sg.p1, lo = sg.lo, all_lo = sg.all_lo;
         const int64_t first = (int64_t)sg.t0 * kPageTile;
@@ -600,7 +613,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
       grid_dependency_wait();  // the exponents
       for (int seg = 0;; ++seg) {
         const Segment& sg = segment(seg);
-        const int n = dead ? 0 : sg.n;
+        const int n = gone() ? 0 : sg.n;
         if (n == 0) break;
         const int p0 = sg.p0, p1 = sg.p1;
         const int ti = h * tb2 + ri;  // token in the block
