@@ -183,3 +183,61 @@ def test_attend_right_behind_an_append_reads_what_it_wrote(dtype, hq, hkv, news)
         got = s.cache.attend(s.q, *pools)
         torch.cuda.synchronize()
         assert torch.equal(got, s.cache.attend(s.q, *pools)), i
+
+
+def _cut(s, lens, offs):
+    """The sequences as the entry points cut them: (tokens, first row, new rows, sequence)."""
+    cap, seqs = s.max_pages * s.page, []
+    for b, n in enumerate(lens):
+        o0 = min(max(offs[b], 0), s.rows)
+        o1 = min(max(offs[b + 1], o0), s.rows)
+        seqs.append((min(max(n, 0), cap), o0, min(o1 - o0, s.max_q), b))
+    return seqs
+
+
+@pytest.mark.parametrize("news,max_q,lens,offs", [
+    (None, 1, [-3, 60], [0, 1, 2]), (None, 1, [81, 60], [0, 1, 2]), (None, 1, [2 ** 31 - 1, 60], [0, 1, 2]),
+    ([2, 2], 2, [-3, 60], [0, 2, 4]), ([2, 2], 2, [81, 60], [0, 2, 4]),
+    ([40, 40], 40, [-2 ** 31, 60], [0, 40, 80]), ([40, 40], 40, [60, 81], [0, 40, 80]),
+    ([40, 40], 50, [60, 60], [0, 90, 80]), ([40, 40], 40, [60, 60], [-4, 30, 60]),
+    ([40, 40], 80, [60, 60], [0, 40, 81]), ([40, 40], 80, [60, 60], [-2 ** 31, 40, 2 ** 31 - 1]),
+    ([40, 40], 40, [60, 60], [0, 45, 50]), ([40, 40], 40, [60, 60], [0, 10, 80]),
+    ([2, 2], 2, [60, 60], [0, 3, 4]), ([40, 40], 80, [60, 60], [0, 80, 40])])
+@pytest.mark.parametrize("what", ["append", "attend"])
+def test_each_length_and_offset_out_of_bounds_is_cut_and_flagged(news, max_q, lens, offs, what):
+    s = Step([60, 60], news, max_q=max_q, seed=44)
+    assert s.max_pages * s.page == 80
+    # the last page of each exists, so that nothing but the length or offset is wrong
+    s.table[:, 4] = sorted(set(range(s.n_pages)) - set(s.table[s.table >= 0].tolist()))
+    s.t_table.copy_(torch.from_numpy(s.table))
+    s.t_lens.copy_(torch.tensor(lens))
+    s.t_offs.copy_(torch.tensor(offs))
+    before = [p.clone() for p in s.pools]
+    out = torch.full((s.rows, s.hq, s.d), 7.0, dtype=s.dtype, device=DEV)
+    if what == "append":
+        s.cache.append(s.K, s.V, *s.pools)
+    else:
+        s.cache.attend(s.q, *s.pools, out=out)
+    torch.cuda.synchronize()
+    assert s.cache.flags() == salsc.FLAG_BAD_INDEX
+    if what == "attend":
+        want, off = np.full(out.shape, 7.0), np.zeros(out.shape)
+        for n, row, m, b in _cut(s, lens, offs):
+            one = dict(s.spec(), lens=[n], offs=[row, row + m], table=[s.table[b].tolist()])
+            ref, tol = po.attend(one, s.q, *s.pools, s.hq, s.dtype)
+            want[row:row + m], off[row:row + m] = ref[row:row + m], tol[row:row + m]
+        assert (np.abs(out.double().cpu().numpy() - want) <= off).all()
+        return
+    scales = [x.cpu().double().numpy() for x in before[2:]]
+    vals = [po.values(p, x) for p, x in zip(before[:2], before[2:])]
+    tols = [np.zeros(v.shape) for v in vals]
+    for n, row, m, b in _cut(s, lens, offs):
+        one = dict(s.spec(), lens=[n], offs=[row, row + m], table=[s.table[b].tolist()])
+        for i, (v, t, sc) in enumerate(po.append(one, s.K, s.V, *before)):
+            for pg in set(np.nonzero(t)[0].tolist()):
+                vals[i][pg], tols[i][pg], scales[i][pg] = v[pg], t[pg], sc[pg]
+    for v, t, sc, pages, got, was in zip(vals, tols, scales, s.pools[:2], s.pools[2:], before):
+        assert np.array_equal(got.cpu().double().numpy(), sc)
+        assert (np.abs(po.values(pages, got) - v)[t > 0] <= t[t > 0]).all()
+        raw, old = (x.view(torch.uint8).cpu().numpy() for x in (pages, was))
+        assert np.array_equal(raw[t == 0], old[t == 0])
