@@ -374,8 +374,8 @@ cudaError_t launch_page_attend(const PageStep& s, const void* q, int64_t q_strid
 size_t page_attend_workspace(const PageStep& s, salsc_dtype dt);
 size_t page_attend_cleared();  // bytes at the workspace's start that are 0 between calls
 // The attention of few rows (page_few.cu): rows of its row blocks, and its launch.
-int page_few_rows(int64_t rows, salsc_dtype dt);  // for sequences of up to `rows` rows
-int page_few_grid(const PageStep& s, int rows, salsc_dtype dt);
+int page_few_rows(int64_t rows);  // for sequences of up to `rows` rows
+int page_few_grid(int rows, salsc_dtype dt);
 cudaError_t launch_page_few(const PageStep& s, const PageWork& w, const void* q, int64_t q_stride,
                             const void* k_pages, const void* v_pages, const float* k_scales,
                             const float* v_scales, void* out, salsc_dtype dt, cudaStream_t stream);

@@ -116,13 +116,13 @@ struct Plan {
 
 Plan make_plan(const PageStep& s, salsc_dtype dt, void* part) {
   Plan p{};
-  int rows = page_few_rows((int64_t)s.max_q * s.G, dt);
+  int rows = page_few_rows((int64_t)s.max_q * s.G);
   p.has_many = dt == SALSC_BF16 && (int64_t)s.max_q * s.G > rows;
-  if (p.has_many) rows = page_few_rows(s.G, dt);
+  if (p.has_many) rows = page_few_rows(s.G);
   // page_few's counters come first, and nothing else lies there whatever the
   // descriptor: salsc_page_prepare clears them, and each call leaves them so
   p.bytes = align_up(page_attend_cleared());
-  p.few = layout(s, rows, page_few_grid(s, rows, dt), part, p.bytes);
+  p.few = layout(s, rows, page_few_grid(rows, dt), part, p.bytes);
   p.few.done = (uint32_t*)part;
   p.few.tb = rows / s.G;
   p.few.over = kOverFew;

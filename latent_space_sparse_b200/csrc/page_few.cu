@@ -273,7 +273,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         };
         for (int seg = 0;; ++seg) {
           const int n = cur.upto(x1);
-        if (n <= 0) break;
+          if (n <= 0) break;
           wait(qready, seg & 1);
           scores(it);
           for (int i = 0; i < n; ++i, ++it) {
@@ -559,22 +559,19 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
         if (warp * 32 < D) {
 #pragma unroll
           for (int r0 = 0; r0 < RC; r0 += 4) {
-            uint32_t v[kT][4];
+            uint32_t v[kT][2][2];
 #pragma unroll
             for (int k = 0; k < kT; ++k) {
-              uint32_t a[2], c[2];
-              tc::tmem_ld2(lanes + 2 * kN + k * RC + r0, a);
-              tc::tmem_ld2(lanes + 2 * kN + k * RC + r0 + 2, c);
-              v[k][0] = a[0], v[k][1] = a[1], v[k][2] = c[0], v[k][3] = c[1];
-              tc::tmem_ld_wait();
-              v[k][0] = a[0], v[k][1] = a[1], v[k][2] = c[0], v[k][3] = c[1];
+              tc::tmem_ld2(lanes + 2 * kN + k * RC + r0, v[k][0]);
+              tc::tmem_ld2(lanes + 2 * kN + k * RC + r0 + 2, v[k][1]);
             }
+            tc::tmem_ld_wait();
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               if (r0 + r < rows) {
-                float a = __uint_as_float(v[kT - 1][r]);
+                float a = __uint_as_float(v[kT - 1][r / 2][r % 2]);
 #pragma unroll
-                for (int k = kT - 2; k >= 0; --k) a = fmaf(a, 1.f / kStep, __uint_as_float(v[k][r]));
+                for (int k = kT - 2; k >= 0; --k) a = fmaf(a, 1.f / kStep, __uint_as_float(v[k][r / 2][r % 2]));
                 a *= 1.f / kPScale;
                 if (whole) {
                   const float ll = wsum[0][r0 + r] + wsum[1][r0 + r] + wsum[2][r0 + r] + wsum[3][r0 + r];
@@ -640,14 +637,13 @@ cudaError_t launch_d(int rc, const PageStep& s, const PageWork& w, const void* q
 
 }  // namespace
 
-int page_few_rows(int64_t want, salsc_dtype dt) {
-  const int most = 16;
+int page_few_rows(int64_t want) {
   int rc = 4;
-  while (rc < most && rc < want) rc *= 2;
+  while (rc < 16 && rc < want) rc *= 2;
   return rc;
 }
 
-int page_few_grid(const PageStep&, int rows, salsc_dtype dt) {
+int page_few_grid(int rows, salsc_dtype dt) {
   const int n = (dt == SALSC_F32 ? kTerms<float> : kTerms<__nv_bfloat16>) * rows;
   return n > 80 ? kPageGrid : 2 * kPageGrid;  // as Few::kCtas
 }

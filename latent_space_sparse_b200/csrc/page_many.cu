@@ -29,7 +29,8 @@
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of a half (a
 // thread per row), warps 8-11 cache tiles (codes to f16), warp 12 issues the
-// MMAs, warp 13 copies queries and pages to shared memory.  Each role's loop is
+// MMAs, warp 13 copies queries and pages to shared memory (warps 14 and 15 are
+// there because registers are shared out by four warps).  Each role's loop is
 // kept short: unrolled over a whole tile they came to 40 KB, and waiting for
 // instructions was the largest stall.
 //
