@@ -269,18 +269,8 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
       __syncwarp();
     }
     if (!live) continue;
-    // earlier codes stand for code * old: whatever its sign, they are recoded
-    // unless it stays (what is not finite becomes NaN)
-    float sc = pow2_scale(a), ratio = 1.f;
-    if (lo > 0) {
-      const float size = fabsf(old);
-      if (size <= 3.402823466e38f) {
-        sc = fmaxf(sc, size);
-        ratio = old / sc;
-      } else {
-        ratio = __uint_as_float(0x7FC00000u);
-      }
-    }
+    float sc = pow2_scale(a);
+    if (fabsf(old) <= 3.402823466e38f) sc = fmaxf(sc, fabsf(old));
     const float inv = 1.f / sc;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -302,7 +292,9 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
         }
         *(uint2*)row = codes8(y[0], inv);
         *(uint2*)(row + kHalf) = codes8(y[1], inv);
-      } else if (slot < lo && ratio != 1.f) {
+      } else if (slot < lo && old != sc) {
+        // earlier codes stand for code * old, whatever its sign (what is not finite becomes NaN)
+        const float ratio = fabsf(old) <= 3.402823466e38f ? old * inv : __uint_as_float(0x7FC00000u);
         *(uint2*)row = recode8(*(const uint2*)row, ratio);
         *(uint2*)(row + kHalf) = recode8(*(const uint2*)(row + kHalf), ratio);
       }
