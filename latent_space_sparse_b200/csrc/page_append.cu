@@ -25,11 +25,12 @@
 // to a CTA keep more loads in flight, with the loads issued before cos and sin
 // are computed.
 //
-// What bounds it: instructions, 60 % of the issue slots, then the latency of the
-// loads.  16.7K tokens of prompts (8 heads of 128, bf16): 27 us, 3.7 TB/s; with
-// sizes taken one by one and fp64 angles it was 47.  Single tokens: 3.5 us for 4
-// sequences of 8 heads, 7.6 for 64 of 32, one dependent load after another
-// (lengths, table, the page's scale beside the new values).
+// What bounds it: instructions, half of the issue slots, and the latency of the
+// loads.  16.7K tokens of prompts (8 heads of 128, bf16): 30 us, 3.3 TB/s (28.6 us
+// from a graph); with sizes taken one by one and fp64 angles it was 47.  Single
+// tokens, from a graph: 3.5 us for 4 sequences of 8 heads, one dependent load after
+// another (lengths, table, the page's scale beside the new values); 7.6 for 64 of 32
+// heads, where an item's threads are those of a whole page and most have no token.
 #include <algorithm>
 
 #include "page.cuh"
@@ -320,9 +321,9 @@ cudaError_t launch(const PageStep& s, const void* K, int64_t k_stride, const voi
   }
   const int per = s.T * D / 32, items = kThreads / per, passes = (2 * s.U + items - 1) / items;
   // Passes of a CTA: so many that it computes one cos and sin a thread for
-  // each (16.7K tokens, pages of 16: four passes 28.8 us, two 29.9, one 33.2);
-  // fewer where the step is small and CTAs would be missing (64 single tokens of
-  // 32 heads: two passes 7.6 us, one 8.9).
+  // each (16.7K tokens, pages of 16, when it was chosen: four passes 28.8 us, two
+  // 29.9, one 33.2); fewer where the step is small and CTAs would be missing (64
+  // single tokens of 32 heads: two passes 7.6 us, one 8.9).
   int64_t part = std::max(1, s.T * (D / 2) / kThreads);
   part = std::min(part, std::max<int64_t>(1, (passes * pages + kTargetCtas - 1) / kTargetCtas));
   const int64_t parts = (passes + part - 1) / part;

@@ -7,9 +7,10 @@ namespace {
 
 constexpr int kMergeWarps = 4, kMergeRows = 4;  // warps of a merge CTA, rows of a warp
 // What a unit takes besides its tiles, in tiles: without it the CTAs with many
-// short units were last (a prompt of 4K 442 us, with it 261 at the time); 1, 2, 3,
-// 4 and 6 for page_few gave 67, 61, 53, 53 and 55 us on 64 short sequences, 2, 3,
-// 4, 6 and 8 for page_many 227, 227, 225, 228 and 232 us on a prompt of 4K.
+// short units were last (a prompt of 4K 442 us, with it 261 at the time). The choice
+// is flat: 1, 2, 3, 4 and 6 for page_few gave 67, 61, 53, 53 and 55 us on 64 short
+// sequences, 2, 3, 4, 6 and 8 for page_many 227, 227, 225, 228 and 232 us on a
+// prompt of 4K (both when they were chosen).
 constexpr int kOverFew = 3, kOverMany = 3;
 
 // A warp takes kMergeRows rows of the unit that CTA c starts (usually of two
@@ -102,12 +103,15 @@ PageWork layout(const PageStep& s, int rows, int grid, void* part, size_t& off) 
 
 // The kernels of a step.  page_few takes sequences of up to 16 rows (new tokens
 // times heads per KV head) and all of fp32 storage, page_many the others: at 16
-// rows page_few takes 62 us and page_many 83 (8 sequences of 8192 tokens, 4 of
-// them new, 32 heads on 8), at 20 rows page_many 49 us and a page_few for 32 rows
-// 95 (4 sequences of 8192, 5 new).  A step that has both
+// rows page_few takes 56 us and page_many 84 (8 sequences of 8192 tokens, 4 of
+// them new, 32 heads on 8; 53 and 84 us for 2 sequences, 16 new, 32 heads on 32),
+// at 20 rows page_many 50 us (4 sequences of 8192, 5 new), where a page_few for 32
+// rows took 95 when there was one.  A step that has both
 // kinds sends page_few the sequences with a single new token only: its time
 // grows with the rows that it is built for (eight requests of 1 to 1024 new
-// tokens: 237 us with one for 32 rows, 208 with one for 4).
+// tokens, when it was chosen: 237 us with one for 32 rows, 208 with one for 4).
+// fp32 storage pays for that rule at prompts: the cache is read once for every 16
+// rows, so that a prompt of 4K takes 2.8 ms, 14 times as long as in bf16.
 struct Plan {
   PageWork few, many;
   bool has_many;

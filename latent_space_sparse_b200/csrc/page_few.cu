@@ -32,8 +32,8 @@
 // dimension), 4 TMA producer (lanes issue a tile's pages), 5 MMA issuer.
 //
 // What bounds it: long caches the read of the codes.  Single tokens of four
-// sequences of 32K (32 heads on 8): 51 us, 5.3 TB/s or 0.80 of the measured
-// copy rate; 16K to 128K: 84 us, 6.0 TB/s or 0.92.  The rest is about 9 us of
+// sequences of 32K (32 heads on 8), replayed from a graph: 50 us, 5.3 TB/s or 0.81
+// of the measured copy rate; 16K to 128K: 84 us, 6.0 TB/s or 0.91.  The rest is about 9 us of
 // start and end: lengths, table, scales and codes one after another from
 // memory, the pipeline's first tile, and the merge.  With one CTA per SM (six
 // tiles in flight instead of three in each of two) 60 and 96 us, and 64 short

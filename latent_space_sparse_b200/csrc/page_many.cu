@@ -42,7 +42,7 @@
 // asks) and values (512); two halves in flight cover each other only in part,
 // and a tile takes 4000 to 4200 cycles where the MMAs alone need 2048 and the
 // exponentials as much: MMA and MUFU pipes 52 % busy, issue slots 37 %.
-// Measured: 2048 tokens at the end of 32K, 32 heads on 8: 1.0 ms, 1.06 PFLOP/s.
+// Measured: 2048 tokens at the end of 32K, 32 heads on 8: 1.05 ms, 1.02 PFLOP/s.
 // Tried and slower: 16 softmax warps with two threads to a row (1.12 ms against
 // 1.08 then), scores by 64 tokens in turn (1.19 against 1.06), the halves taking
 // turns at the exponentials (1.16 against 1.06).
