@@ -270,9 +270,19 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
       __syncwarp();
     }
     if (!live) continue;
-    float sc = pow2_scale(a);
-    if (fabsf(old) <= 3.402823466e38f) sc = fmaxf(sc, fabsf(old));
-    const float inv = 1.f / sc;
+    old += old - old;  // NaN if it is not finite: then it does not count, and earlier codes become NaN
+    const float sc = fmaxf(pow2_scale(a), fabsf(old)), inv = 1.f / sc;
+    if (lo > 0 && old != sc) {  // earlier codes stand for code * old, whatever its sign
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int ch = ti + k * per, slot = ch / kRowChunks, i0 = ch % kRowChunks * 8;
+        uint8_t* row = page + slot * D + i0;
+        if (slot < lo) {
+          *(uint2*)row = recode8(*(const uint2*)row, old * inv);
+          *(uint2*)(row + kHalf) = recode8(*(const uint2*)(row + kHalf), old * inv);
+        }
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int ch = ti + k * per, slot = ch / kRowChunks, i0 = ch % kRowChunks * 8;
@@ -293,11 +303,6 @@ page_append_kernel(const __grid_constant__ PageStep s, const T* __restrict__ K, 
         }
         *(uint2*)row = codes8(y[0], inv);
         *(uint2*)(row + kHalf) = codes8(y[1], inv);
-      } else if (slot < lo && old != sc) {
-        // earlier codes stand for code * old, whatever its sign (what is not finite becomes NaN)
-        const float ratio = fabsf(old) <= 3.402823466e38f ? old * inv : __uint_as_float(0x7FC00000u);
-        *(uint2*)row = recode8(*(const uint2*)row, ratio);
-        *(uint2*)(row + kHalf) = recode8(*(const uint2*)(row + kHalf), ratio);
       }
     }
     if (ti == 0) *scales = sc;
