@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from latent_space_sparse_b200 import salsc
+from latent_space_sparse_b200 import salsc, synth, workloads
 from tests import page_oracle as po
 from tests.test_page_gpu import BF16, DEV, F32, Step, check_append, check_attend
 
@@ -241,3 +241,46 @@ def test_each_length_and_offset_out_of_bounds_is_cut_and_flagged(news, max_q, le
         assert (np.abs(po.values(pages, got) - v)[t > 0] <= t[t > 0]).all()
         raw, old = (x.view(torch.uint8).cpu().numpy() for x in (pages, was))
         assert np.array_equal(raw[t == 0], old[t == 0])
+
+
+@pytest.mark.parametrize("news", [None, [200, 1, 9]])
+@pytest.mark.parametrize("graph", [False, True])
+def test_compressed_and_full_layers_take_turns_on_one_stream(news, graph):
+    """A model's layers: latent decode steps and paged steps one after another, launched early on
+    each other's heels, give what each gives alone."""
+    w = workloads.Workload(name="layers", batch=2, n_q_heads=8, n_kv_heads=2, head_dim=128, rank=128,
+                           top_k=256, seq_lens=(1500, 700), dtype="bf16", rope_base=10000.0,
+                           low_rank=16, seed=62)
+    x = {k: v.to(DEV) for k, v in synth.decode_inputs(w).items() if k in ("q", "Kc", "Vc", "Pk", "Pv")}
+    dec = salsc.Decoder(w.batch, w.n_q_heads, w.n_kv_heads, w.head_dim, w.rank, w.top_k, w.seq_lens,
+                        rope_base=w.rope_base, dtype=BF16, device=DEV)
+    s = Step([1200, 900, 309], news, seed=50)
+    s.cache.append(s.K, s.V, *s.pools)
+    torch.cuda.synchronize()
+    latent = dec.step(**x)
+    torch.cuda.synchronize()
+    full = s.cache.attend(s.q, *s.pools)
+    torch.cuda.synchronize()
+    a, b = ([torch.zeros_like(t) for _ in range(6)] for t in (latent, full))
+
+    def layers():
+        for i in range(6):
+            s.cache.append(s.K, s.V, *s.pools)  # the same tokens again
+            s.cache.attend(s.q, *s.pools, out=b[i])
+            dec.step(**x, out=a[i])
+
+    if graph:
+        layers()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layers()
+        for t in a + b:
+            t.zero_()
+        g.replay()
+        g.replay()
+    else:
+        layers()
+    torch.cuda.synchronize()
+    assert dec.flags() == 0 and s.cache.flags() == 0
+    assert all(torch.equal(t, latent) for t in a)
+    assert all(torch.equal(t, full) for t in b)
