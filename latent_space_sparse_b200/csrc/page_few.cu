@@ -143,12 +143,14 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
     tc::mbar_init(drained, 1);
     tc::mbar_fence_init();
   }
-  if (warp == 5) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
   if (warp == 4 && lane < 2) tc::tma_prefetch_desc(lane ? &vmap : &kmap);
   // Behind page_many, which runs on other sequences and starts when all that
   // came before the step is done: this kernel's CTAs start where its CTAs have
   // ended, and wait for all of them at their own end.
   if (!w.overlaps) grid_dependency_wait();
+  // (tensor memory last: a kernel before that starts to allocate must not find it taken
+  // by one that waits for it)
+  if (warp == 5) tc::tmem_alloc(tc::smem_u32(&tmem_base), C::kTmem);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
