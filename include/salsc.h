@@ -519,10 +519,9 @@ salsc_status salsc_page_append(const salsc_page_desc* desc, const void* K_new, i
  * NaN or infinity in a query makes its row NaN; a NaN in a key, and a scale that
  * is not finite, of tokens that a row sees make the row NaN, a NaN in a value at
  * least that dimension of it.
- * Scales may have any sign.  Value scales keep their accuracy from 2^-99 on, and
- * beside each other in one row where they lie within 2^100; below 2^-99 values
- * count as zeros, whose tokens keep their weight beside value scales from 2^-60
- * to 2^50.
+ * Scales may have any sign.  Value scales keep their accuracy from 2^-100 on, and
+ * beside each other in one row where they lie within 2^100 (those of 2^-100 and
+ * less, which pages of zeros have, beside any).
  *
  * Accuracy: products of codes are exact and sums are fp32.  Of the elements of a
  * query and of the weights of a row, fp32 storage keeps 24 bits, bf16 storage 11

@@ -172,16 +172,22 @@ __device__ __forceinline__ void page_cs(int pos, uint64_t turns, float& c, float
 // ---------------------------------------------------------------- attention
 
 // A page's value scale as f * 2^e.  Finite scales from 2^-99 on have 1 <= |f| < 2.
-// Smaller ones, which the append writes for pages of zeros, are zero beside
-// anything else: they take an e in the middle, so that such a page keeps its place
-// in the normaliser beside scales from 2^-60 to 2^50 and hides none of their values.
-// What is not finite is NaN.  down = 2^-e.
+// Smaller ones, which the append writes for pages of zeros, would have weights of
+// 2^-126 and less beside scales above 2^26 and drop out of the normaliser: they take
+// an e that lies 24 below the largest, `big`, that was met so far (-100 at least,
+// which leaves them exact where nothing larger is).  What is not finite is NaN.
+// down = 2^-e.
 struct ValueScale {
   float f, e, down;
 };
-__device__ __forceinline__ ValueScale value_scale(float v) {
+constexpr int kNoScale = -1000;  // no scale from 2^-99 on was met
+__device__ __forceinline__ int scale_exponent(float v) {
   const int ex = (int)((__float_as_uint(v) >> 23) & 255u);
-  const int e = ex < 28 ? -50 : ex - 127;
+  return ex < 28 || ex == 255 ? kNoScale : ex - 127;
+}
+__device__ __forceinline__ ValueScale value_scale(float v, int big) {
+  const int ex = (int)((__float_as_uint(v) >> 23) & 255u);
+  const int e = ex < 28 ? max(big - 24, -100) : ex - 127;
   const float down = __uint_as_float(e == 127 ? 0x00400000u : (uint32_t)(127 - e) << 23);
   if (ex == 255) return ValueScale{__uint_as_float(0x7FC00000u), 0.f, 1.f};
   return ValueScale{v * down, (float)e, down};
@@ -313,6 +319,15 @@ __device__ __forceinline__ bool page_begin(PageCursor& c, int64_t& total, int64_
   return true;
 }
 
+// A piece's factor 2^(m_i - m), with l += 2^(m_i - m) l_i. In two steps: pieces of
+// small value scales have a large l_i and an m_i far below. A piece without a token
+// (m_i = -inf) weighs nothing; a NaN stays one.
+__device__ __forceinline__ float page_factor(float2 ml, float m, float& l) {
+  const float h = ml.x == -INFINITY ? 0.f : exp2f(0.5f * (ml.x - m));
+  l += h * ml.y * h;
+  return h * h;
+}
+
 // One row of a unit whose pieces are those of CTAs c0 .. c0 + n - 1:
 //   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i
 // CTA c0's second slot holds the unit's first piece, the following CTAs' first
@@ -334,9 +349,7 @@ __device__ __forceinline__ void page_merge_row(const PageWork& w, int c0, int n,
     float f = 0.f;
     if (i0 + lane < n) {
       const float2 ml = __ldcg(&w.ml[slot(i0 + lane)]);
-      // a piece without a token (m = -inf) weighs nothing; a NaN stays one
-      f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      l += f * ml.y;
+      f = page_factor(ml, m, l);
     }
     const int top = min(32, n - i0);
 #pragma unroll 8

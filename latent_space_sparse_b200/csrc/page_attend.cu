@@ -43,9 +43,7 @@ page_merge_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pa
     float f = 0.f;
     if (i0 + mp < n) {
       const float2 ml = w.ml[slot(i0 + mp, rr)];
-      // a piece without a token (m = -inf) weighs nothing; a NaN stays one
-      f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      l += f * ml.y;
+      f = page_factor(ml, m, l);
     }
     const int top = min(kPieces, n - i0);
 #pragma unroll 2

@@ -182,7 +182,7 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           const bool need = tile + lane / npg < n && first <= hi && first + s.T > lo;
           return need ? page_of<true>(s, cur.b, (int)(first / s.T)) : -1;
         };
-        int pg = look(0);
+        int pg = look(0), big = kNoScale;
         float ks = 0.f, vs = 0.f;
         if (pg >= 0) {
           ks = __ldcg(k_scales + (size_t)pg * s.U + cur.u);
@@ -209,8 +209,9 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
               tc::tma_load_2d(dst, &kmap, 0, row, kfull(st));
               tc::tma_load_2d(dst + kTile, &vmap, 0, row, vfull(st));
             }
+            big = max(big, __reduce_max_sync(0xffffffffu, mine ? scale_exponent(vs) : kNoScale));
             if (mine) {
-              const ValueScale v = value_scale(vs);
+              const ValueScale v = value_scale(vs, big);
               meta[st].ks[sub] = key_scale(ks);
               meta[st].vf[sub] = v.f;
               meta[st].ve[sub] = v.e;
@@ -485,8 +486,10 @@ page_few_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Page
           if (grew) {
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
-              al[r] = al[r] == m[r] ? 1.f : ex2(al[r] - m[r]);
-              l[r] *= al[r];
+              // in two steps, as page_factor
+              const float h = al[r] == m[r] ? 1.f : ex2(0.5f * (al[r] - m[r]));
+              l[r] = l[r] * h * h;
+              al[r] = h * h;
             }
             if (i > 0) {  // the sums so far (of this piece) follow the maximum
               wait(pvdone(buf ^ 1), ((it - 1) >> 1) & 1);

@@ -403,7 +403,7 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const int64_t first = (int64_t)(t0 + i) * kPageTile + ((lane & 7) * 16 & -s.T);
             return i < n && first <= hi && first + s.T > lo ? page_of<true>(s, cur.b, (int)(first / s.T)) : -1;
           };
-          int pg = look(0);
+          int pg = look(0), big = kNoScale;
           float ks = 0.f, vs = 0.f;
           auto scales = [&] {
             ks = vs = 0.f;
@@ -421,7 +421,8 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
             const bool first = lane < 8 && (lane * 16) % s.T == 0 && pg >= 0;
             const int src = (pg * s.U + cur.u) * s.T;
             const uint32_t dst = sm0 + C::kOffCodes + lane * 16 * D;
-            const ValueScale v = value_scale(vs);
+            big = max(big, __reduce_max_sync(0xffffffffu, scale_exponent(vs)));
+            const ValueScale v = value_scale(vs, big);
             const bool plain = __all_sync(0xffffffffu, pg < 0 || v.f == 1.f);
             wait(cfree(0), (it & 1) ^ 1);
             if (gone()) break;
@@ -715,9 +716,9 @@ page_many_kernel(const __grid_constant__ PageStep s, const __grid_constant__ Pag
               const float top = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
               const bool none = m == -INFINITY;
               const float by = top > kUp || (none && top > -INFINITY) ? top - kUp : 0.f;
-              const float al = none ? 0.f : ex2(-by);
+              const float half = none ? 0.f : ex2(-0.5f * by), al = half * half;
               if (!none || top > -INFINITY) m = (none ? 0.f : m) + by;
-              l *= al;
+              l = l * half * half;  // in two steps, as page_factor
 #pragma unroll
               for (int j = 0; j < kPageTile; ++j) t[j] -= by;
               if (i > 0) {  // the sums so far (of this piece) follow

@@ -71,7 +71,8 @@ def test_append_behind_a_page_scale_of_any_kind_keeps_the_earlier_tokens(dtype, 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("news", [None, [3, 2], [150, 90]])
 @pytest.mark.parametrize("zero,rest", [(-100, 30), (-100, 50), (-100, -60), (-60, 40), (-99, 0), (119, 119),
-                                       (119, 20), (120, 120), (127, 127), (127, 30)])
+                                       (119, 20), (120, 120), (127, 127), (127, 30), (-100, -99), (-100, -80),
+                                       (-100, 120), (-100, 127), (-101, -101), (-99, -99), (-101, -98)])
 def test_attend_value_scales_far_apart(dtype, news, zero, rest):
     """Pages of zeros beside pages of any magnitude (the append gives them a scale of 2^-100), and
     value scales far from one."""
@@ -81,8 +82,10 @@ def test_attend_value_scales_far_apart(dtype, news, zero, rest):
     s.pools[3] = torch.where(small[:, None], 2.0 ** zero, 2.0 ** rest).float().expand(-1, s.hkv).contiguous()
     if zero == -100:
         s.pools[1].view(torch.uint8)[small] = 0
+    elif zero == -101:  # the append's scale for zeros and the smallest values
+        s.pools[3].clamp_(min=2.0 ** -100)
     if max(zero, rest) > 100:  # values that stay finite in bf16
-        top = 200.0 if zero < 127 else 1.5
+        top = 200.0 if max(zero, rest) < 127 else 1.5
         s.pools[1] = s.pools[1].float().clamp(-top, top).to(torch.float8_e4m3fn)
     check_attend(s)
 
