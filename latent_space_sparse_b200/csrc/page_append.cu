@@ -26,7 +26,7 @@
 // are computed.
 //
 // What bounds it: instructions, half of the issue slots, and the latency of the
-// loads.  16.7K tokens of prompts (8 heads of 128, bf16): 30 us, 3.3 TB/s (28.6 us
+// loads.  16.7K tokens of prompts (8 heads of 128, bf16): 30 us, 3.3 TB/s (28.2 us
 // from a graph); with sizes taken one by one and fp64 angles it was 47.  Single
 // tokens, from a graph: 3.5 us for 4 sequences of 8 heads, one dependent load after
 // another (lengths, table, the page's scale beside the new values); 7.6 for 64 of 32

@@ -101,8 +101,8 @@ PageWork layout(const PageStep& s, int rows, int grid, void* part, size_t& off) 
 
 // The kernels of a step.  page_few takes sequences of up to 16 rows (new tokens
 // times heads per KV head) and all of fp32 storage, page_many the others: at 16
-// rows page_few takes 56 us and page_many 84 (8 sequences of 8192 tokens, 4 of
-// them new, 32 heads on 8; 53 and 84 us for 2 sequences, 16 new, 32 heads on 32),
+// rows page_few takes 53 us and page_many 84 (8 sequences of 8192 tokens, 4 of
+// them new, 32 heads on 8; 53 and 83 us for 2 sequences, 16 new, 32 heads on 32),
 // at 20 rows page_many 50 us (4 sequences of 8192, 5 new), where a page_few for 32
 // rows took 95 when there was one.  A step that has both
 // kinds sends page_few the sequences with a single new token only: its time
